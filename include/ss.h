@@ -370,8 +370,9 @@ SS_API int ss_ssd_fwd_path(void);
 
 /*
  * Device fault word of the kernels that bound their waits (the tcgen05 SSD
- * forward): 0 when no wait ran out since the last clear; bit 0 a copy-wait
- * timeout, bit 1 a product-wait timeout, bit 2 a drain timeout at exit.
+ * kernels) or take indexes from device memory: 0 when nothing went wrong since
+ * the last clear; bit 0 a copy-wait timeout, bit 1 a product-wait timeout,
+ * bit 2 a drain timeout at exit, bit 3 a bad sequence offset or cache slot.
  * Synchronizes the current device first; clear != 0 resets the word.
  * Returns -1 (and sets ss_last_error) when the device reports an error.
  */
@@ -439,6 +440,147 @@ SS_API ss_status ss_state_update(int64_t batch, int64_t dim, int64_t dstate, int
                           const float* A, const void* B, const void* C, const float* D,
                           const float* delta_bias, int delta_softplus, void* y,
                           void* stream);
+
+/*
+ * ---- Time-major operators around the SSD scan (Mamba-2) --------------------
+ * What a Mamba-2 layer runs between its two projections, on the input
+ * projection's rows as it writes them (one row per token, columns
+ * [z | x B C | dt]): the causal convolution with its SiLU (training and
+ * prompts), the scan of prompts on a cache of states, the step of one token
+ * per request, and the gated norm.  "Mamba" (stanleyjacob.dev), Part IV
+ * Stages 2 and 7 and Part V ("Mamba-2 and state-space duality").
+ *
+ * Common to these calls:
+ *   - Rows: an argument `ldX` is the distance, in elements, between the rows of
+ *     X (>= the row's width; inside a row elements are contiguous), so column
+ *     slices of a wider array are taken as they are.  Arrays without an ld are dense.
+ *   - Ragged sequences: `tokens` rows hold nseq sequences, sequence i the rows
+ *     [cu_seqlens[i], cu_seqlens[i+1]) with cu_seqlens (nseq + 1,) int32 in
+ *     device memory, or tokens / nseq rows each when cu_seqlens is NULL.  A
+ *     sequence may be empty.  Rows of no sequence are not used, and outputs' are not written.
+ *     Offsets that decrease or leave [0, tokens] are clamped (no access out of
+ *     range; the affected sequences' results mean nothing) and set bit 3 of ss_device_fault.
+ *   - State caches: sequence (or request) i uses slot slots[i] of a cache of
+ *     nslots slots, slots (nseq,) int32 in device memory, or slot i when slots
+ *     is NULL.  A negative slot marks padding: the sequence's rows of the
+ *     outputs and all states are left as they were.  A slot >= nslots, or one
+ *     that an earlier sequence of the same call has, is treated as padding too,
+ *     and sets bit 3 of ss_device_fault: no two sequences ever share a state in
+ *     a call.  fresh (nseq,) uint8, or NULL: nonzero starts the sequence from
+ *     a zero state instead of its slot's.  Only slots in use are read or written.
+ *   - Launches depend on the arguments' sizes only, never on device data: the
+ *     calls capture into CUDA graphs, and a replay follows the data then in
+ *     cu_seqlens, slots and fresh.
+ *   - A NaN or an infinity in one sequence never reaches another's results.
+ *   - Sizes: tokens < 2^31 - 2^16, nseq <= 2^20, batch <= 65535; tokens, nseq,
+ *     rows and batch may be 0.
+ */
+
+/*
+ * Causal depthwise conv1d (+ SiLU) of a packed row, split into its pieces:
+ *   y[t,c] = silu(bias[c] + sum_{k<W} w[c,k] xin[t-(W-1)+k, c])
+ * xin is x inside the token's sequence, before its start the slot's window (or
+ * zero).  Columns [0, dim0) go to y0 (tokens, dim0), the next dim1 to y1, the
+ * last dim2 to y2; dim1 and dim2 may be 0 (their pointers NULL).
+ *   x (tokens, dim) dtype, rows ldx apart;  w (dim, width) fp32, width 1..4;
+ *   bias (dim,) fp32 or NULL;  silu 0 leaves the SiLU out
+ *   state (nslots, dim, width-1) fp32 in/out: a sequence's last width-1 inputs,
+ *   oldest first, as ss_conv1d_fwd keeps them; nslots 0: no cache.
+ */
+SS_API ss_status ss_conv1d_tm_fwd(int64_t tokens, int64_t nseq, int64_t dim, int64_t width, int dtype,
+                                  const void* x, int64_t ldx, const float* w, const float* bias,
+                                  const int32_t* cu_seqlens, float* state, int64_t nslots,
+                                  const int32_t* slots, const uint8_t* fresh, int silu, int64_t dim0,
+                                  int64_t dim1, int64_t dim2, void* y0, void* y1, void* y2, void* stream);
+
+/* Bytes of device workspace ss_conv1d_tm_bwd needs.  (size_t)-1 on invalid arguments. */
+SS_API size_t ss_conv1d_tm_bwd_workspace_size(int64_t tokens, int64_t dim, int64_t width);
+
+/*
+ * Adjoint of ss_conv1d_tm_fwd without a cache, for the loss sum_i <dy_i, y_i>:
+ *   dx (tokens, dim) dtype, rows lddx apart;  dw (dim, width), dbias (dim,) fp32
+ *   (dbias may be NULL), summed over the tokens of all sequences in a fixed order.
+ * All overwritten; rows of dx in no sequence become zero, their true gradient.
+ */
+SS_API ss_status ss_conv1d_tm_bwd(int64_t tokens, int64_t nseq, int64_t dim, int64_t width, int dtype,
+                                  const void* x, int64_t ldx, const float* w, const float* bias,
+                                  const int32_t* cu_seqlens, int silu, int64_t dim0, int64_t dim1,
+                                  int64_t dim2, const void* dy0, const void* dy1, const void* dy2, void* dx,
+                                  int64_t lddx, float* dw, float* dbias, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace ss_ssd_prefill needs.  (size_t)-1 on invalid arguments. */
+SS_API size_t ss_ssd_prefill_workspace_size(int64_t tokens, int64_t nseq, int64_t nheads, int64_t headdim,
+                                            int64_t ngroups, int64_t dstate);
+
+/*
+ * The SSD scan of ragged sequences on a cache of states (the recurrence of
+ * ss_ssd_fwd; prompts, or pieces of prompts, of a serving batch):
+ *   x, y (tokens, nheads, headdim);  dt (tokens, nheads);
+ *   B, C (tokens, ngroups, dstate);  z like x or NULL (no gate)      dtype bf16 or fp16
+ *   A, D, dt_bias (nheads,) fp32; D, dt_bias may be NULL
+ *   state (nslots, nheads, headdim, dstate) fp32 in/out, 16-byte aligned, or
+ *   NULL: every sequence starts from zero and no end state is kept.
+ * headdim 64, dstate 64 or 128 (else SS_ERR_UNSUPPORTED).  Rows of x, B and C
+ * start on 16-byte boundaries (a multiple of 8 elements apart), y and the
+ * workspace are 16- and 256-byte aligned (else SS_ERR_ALIGNMENT).
+ */
+SS_API ss_status ss_ssd_prefill(int64_t tokens, int64_t nseq, int64_t nheads, int64_t headdim,
+                                int64_t ngroups, int64_t dstate, int dtype, const void* x, int64_t ldx,
+                                const void* dt, int64_t lddt, const float* A, const void* B, int64_t ldb,
+                                const void* C, int64_t ldc, const float* D, const void* z, int64_t ldz,
+                                const float* dt_bias, int dt_softplus, const int32_t* cu_seqlens,
+                                float* state, int64_t nslots, const int32_t* slots, const uint8_t* fresh,
+                                void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace ss_ssd_step needs.  (size_t)-1 on invalid arguments. */
+SS_API size_t ss_ssd_step_workspace_size(int64_t batch, int64_t nheads, int64_t headdim, int64_t ngroups,
+                                         int64_t dstate);
+
+/*
+ * One token of each request: the convolution's step on the packed row x|B|C,
+ * then one step of the SSD recurrence, both on cached states, in place.
+ *   xbc (batch, nheads headdim + 2 ngroups dstate);  dt (batch, nheads);
+ *   z (batch, nheads headdim) or NULL (no gate);  y (batch, nheads, headdim)   dtype
+ *   w, conv_bias: as in ss_conv1d_tm_fwd;  A, D, dt_bias (nheads,) fp32, the last two or NULL
+ *   conv_state (nslots, conv dim, width-1), state (nslots, nheads, headdim,
+ *   dstate) fp32 in/out (conv_state NULL only when width == 1)
+ * headdim 64, dstate 64 or 128; any storage dtype.  The convolution's outputs
+ * stay fp32 on the way to the scan.  Calls that overlap need workspaces of their own.
+ */
+SS_API ss_status ss_ssd_step(int64_t batch, int64_t nheads, int64_t headdim, int64_t ngroups, int64_t dstate,
+                             int64_t width, int dtype, const void* xbc, int64_t ldx, const void* dt,
+                             int64_t lddt, const float* w, const float* conv_bias, int silu, const float* A,
+                             const float* D, const void* z, int64_t ldz, const float* dt_bias,
+                             int dt_softplus, float* conv_state, float* state, int64_t nslots,
+                             const int32_t* slots, void* y, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * Gated RMS norm of each row's groups of `group` columns (group divides dim,
+ * group <= 8192).  s(z) = z sigmoid(z), or 1 when z is NULL:
+ *   gate_last 0:  v = x s(z),  y = v rstd w          rstd = 1 / sqrt(mean(v^2) + eps)
+ *   gate_last 1:  v = x,       y = v rstd w s(z)
+ *   x, z, y (rows, dim) dtype;  w (dim,) fp32;  rstd (rows, dim / group) fp32,
+ *   written for the backward, or NULL.
+ */
+SS_API ss_status ss_gated_norm_fwd(int64_t rows, int64_t dim, int64_t group, int dtype, const void* x,
+                                   int64_t ldx, const void* z, int64_t ldz, const float* w, float eps,
+                                   int gate_last, void* y, float* rstd, void* stream);
+
+/* Bytes of device workspace ss_gated_norm_bwd needs.  (size_t)-1 on invalid arguments. */
+SS_API size_t ss_gated_norm_bwd_workspace_size(int64_t rows, int64_t dim, int64_t group);
+
+/*
+ * Adjoint of ss_gated_norm_fwd for <dy, y>, with its rstd: dx, dz (rows, dim)
+ * dtype, rows lddx, lddz apart (dz required iff z is given); dw (dim,) fp32,
+ * summed over the rows in a fixed order.  All overwritten.
+ */
+SS_API ss_status ss_gated_norm_bwd(int64_t rows, int64_t dim, int64_t group, int dtype, const void* x,
+                                   int64_t ldx, const void* z, int64_t ldz, const float* w,
+                                   const float* rstd, const void* dy, int gate_last, void* dx, int64_t lddx,
+                                   void* dz, int64_t lddz, float* dw, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,8 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
+#include <utility>
 
 #include "../../include/ss.h"
 #include "ss_internal.h"
@@ -220,7 +222,7 @@ bool rows_vec_ok(int64_t seqlen, int dtype, std::initializer_list<const void*> p
 
 extern "C" {
 
-int ss_version(void) { return 1 * 10000 + 4 * 100 + 0; }
+int ss_version(void) { return 1 * 10000 + 5 * 100 + 0; }
 
 const char* ss_last_error(void) { return g_err; }
 
@@ -672,7 +674,12 @@ int ss_ssd_fwd_path(void) {
 
 int ss_device_fault(int clear) {
   unsigned bits = 0;
-  const cudaError_t e = ss::read_tc_fault(&bits, clear != 0);
+  cudaError_t e = ss::read_tc_fault(&bits, clear != 0);
+  for (auto read : {ss::read_fault_conv_tm, ss::read_fault_step, ss::read_fault_prefill}) {
+    unsigned more = 0;
+    if (e == cudaSuccess) e = read(&more, clear != 0);
+    bits |= more;
+  }
   if (e != cudaSuccess) {
     fail(SS_ERR_CUDA, "ss_device_fault: %s", cudaGetErrorString(e));
     return -1;
@@ -777,6 +784,383 @@ ss_status ss_conv1d_step(int64_t batch, int64_t dim, int64_t width, int dtype, f
     return fail(SS_ERR_CUDA, "%s: launch failure injected by SS_FAIL_LAUNCH (nothing enqueued)", __func__);
   cudaError_t e = ss::launch_conv(p, 2, static_cast<ss::DType>(dtype), false, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(SS_ERR_CUDA, "ss_conv1d_step: launch failed: %s", cudaGetErrorString(e));
+  return SS_OK;
+}
+
+// ---- time-major (Mamba-2) operators around the SSD scan --------------------
+namespace {
+
+constexpr int64_t kMaxTokens = INT32_MAX - 65536;  // tile and token arithmetic stays in 31 bits
+
+// Packed sequences and the optional cache they use.
+ss_status check_ragged(const char* fn, int64_t tokens, int64_t nseq, const int32_t* cu_seqlens, bool cache,
+                       int64_t nslots, const int32_t* slots, ss::Ragged* r, ss::Slots* c) {
+  if (tokens < 0 || nseq < 0) return fail(SS_ERR_INVALID_ARG, "%s: tokens and nseq must not be negative", fn);
+  if (tokens > kMaxTokens || nseq > (1 << 20))
+    return fail(SS_ERR_UNSUPPORTED, "%s: sizes beyond the supported range (tokens < 2^31 - 2^16, nseq <= 2^20)", fn);
+  if (!cu_seqlens && nseq > 0 && tokens % nseq)
+    return fail(SS_ERR_INVALID_ARG, "%s: without cu_seqlens, nseq=%lld must divide tokens=%lld", fn, (long long)nseq,
+                (long long)tokens);
+  if (cu_seqlens && !aligned(cu_seqlens, 4)) return fail(SS_ERR_ALIGNMENT, "%s: cu_seqlens not 4-byte aligned", fn);
+  r->cu = cu_seqlens;
+  r->nseq = (int)nseq;
+  r->tokens = (int)tokens;
+  r->seqlen = nseq > 0 ? (int)(tokens / nseq) : 0;
+  if (cache) {
+    if (nslots <= 0 || nslots > INT32_MAX) return fail(SS_ERR_INVALID_ARG, "%s: nslots=%lld", fn, (long long)nslots);
+    if (!slots && nslots < nseq)
+      return fail(SS_ERR_INVALID_ARG, "%s: without slots, the cache needs one slot per sequence (%lld < %lld)", fn,
+                  (long long)nslots, (long long)nseq);
+    if (slots && !aligned(slots, 4)) return fail(SS_ERR_ALIGNMENT, "%s: slots not 4-byte aligned", fn);
+    c->index = slots;
+    c->count = (int)nslots;
+  }
+  return SS_OK;
+}
+
+ss_status check_rows(const char* fn, const char* name, const void* p, int64_t ld, int64_t width, size_t es,
+                     int64_t rows) {
+  if (rows > 0 && !p) return fail(SS_ERR_INVALID_ARG, "%s: %s is required", fn, name);
+  if (ld < width)
+    return fail(SS_ERR_INVALID_ARG, "%s: rows of %s are %lld elements apart but %lld wide", fn, name, (long long)ld,
+                (long long)width);
+  if (p && !aligned(p, es)) return fail(SS_ERR_ALIGNMENT, "%s: %s not aligned to %zu bytes", fn, name, es);
+  return SS_OK;
+}
+
+bool vec_rows(const void* p, int64_t ld, size_t es) { return !p || (aligned(p, 16) && (size_t)ld * es % 16 == 0); }
+
+ss_status check_conv_tm(const char* fn, int64_t dim, int64_t width, int dtype, int64_t dim0, int64_t dim1,
+                        int64_t dim2) {
+  ss_status st = check_dtype(dtype);
+  if (st != SS_OK) return st;
+  if (width < 1 || width > 4)
+    return fail(SS_ERR_UNSUPPORTED, "%s: width=%lld (supported: 1..4)", fn, (long long)width);
+  if (dim <= 0 || dim0 <= 0 || dim1 < 0 || dim2 < 0 || (dim1 == 0 && dim2 > 0) || dim0 + dim1 + dim2 != dim)
+    return fail(SS_ERR_INVALID_ARG, "%s: dim=%lld must be the sum of its pieces (%lld, %lld, %lld), empty ones last",
+                fn, (long long)dim, (long long)dim0, (long long)dim1, (long long)dim2);
+  if (dim > (1 << 22)) return fail(SS_ERR_UNSUPPORTED, "%s: dim above 2^22", fn);
+  return SS_OK;
+}
+
+// Backward strips of the token axis: long enough that the W-1 tokens behind a
+// strip, computed twice, are a few percent; at most 256 strips bound the partials.
+void conv_tm_strips(int64_t tokens, int* strip, int* nstrip) {
+  int64_t len = (tokens + 255) / 256;
+  if (len < 32) len = 32;
+  *strip = (int)len;
+  *nstrip = (int)((tokens + len - 1) / len);
+}
+
+// Backward blocks per column group: about four per SM of a 148-SM device in all.
+int norm_blocks(int64_t rows, int64_t dim, int64_t group, int slots) {
+  const int64_t ngroups = dim / group;
+  int64_t cap = 592 / ngroups;
+  if (cap < 1) cap = 1;
+  const int64_t need = (rows + slots - 1) / slots;
+  return (int)(need < cap ? need : cap);
+}
+
+ss_status check_norm(const char* fn, int64_t rows, int64_t dim, int64_t group) {
+  if (rows < 0 || dim <= 0 || group <= 0 || dim % group)
+    return fail(SS_ERR_INVALID_ARG, "%s: group=%lld must divide dim=%lld (rows=%lld)", fn, (long long)group,
+                (long long)dim, (long long)rows);
+  if (group > ss::kMaxNormGroup)
+    return fail(SS_ERR_UNSUPPORTED, "%s: group=%lld above %d", fn, (long long)group, ss::kMaxNormGroup);
+  if (rows > kMaxTokens || dim > (1 << 22) || dim / group > 65535 || rows * (dim / group) > INT32_MAX)
+    return fail(SS_ERR_UNSUPPORTED, "%s: sizes beyond the supported range", fn);
+  return SS_OK;
+}
+
+}  // namespace
+
+ss_status ss_conv1d_tm_fwd(int64_t tokens, int64_t nseq, int64_t dim, int64_t width, int dtype, const void* x,
+                           int64_t ldx, const float* w, const float* bias, const int32_t* cu_seqlens, float* state,
+                           int64_t nslots, const int32_t* slots, const uint8_t* fresh, int silu, int64_t dim0,
+                           int64_t dim1, int64_t dim2, void* y0, void* y1, void* y2, void* stream) {
+  const char* fn = "ss_conv1d_tm_fwd";
+  ss::ConvTmParams p{};
+  ss_status st = check_conv_tm(fn, dim, width, dtype, dim0, dim1, dim2);
+  if (st != SS_OK) return st;
+  if ((st = check_ragged(fn, tokens, nseq, cu_seqlens, nslots != 0, nslots, slots, &p.seq, &p.slots)) != SS_OK)
+    return st;
+  const size_t es = elt_size(dtype);
+  if ((st = check_rows(fn, "x", x, ldx, dim, es, tokens)) != SS_OK) return st;
+  if (nslots != 0 && width > 1 && !state) return fail(SS_ERR_INVALID_ARG, "%s: nslots given without state", fn);
+  if (!w || (tokens > 0 && (!y0 || (dim1 && !y1) || (dim2 && !y2))))
+    return fail(SS_ERR_INVALID_ARG, "%s: w and an output per piece are required", fn);
+  for (const void* q : {(const void*)y0, (const void*)y1, (const void*)y2})
+    if (q && !aligned(q, es)) return fail(SS_ERR_ALIGNMENT, "%s: output %p not aligned to %zu bytes", fn, q, es);
+  for (const void* q : {(const void*)w, (const void*)bias, (const void*)state})
+    if (q && !aligned(q, 4)) return fail(SS_ERR_ALIGNMENT, "%s: fp32 pointer %p not 4-byte aligned", fn, q);
+  if (nseq == 0) return SS_OK;
+  int sms = 0;
+  if (current_sm_count(&sms) != 0) return fail(SS_ERR_CUDA, "%s: cannot query the device", fn);
+  p.slots.fresh = fresh;
+  p.dim = (int)dim; p.width = (int)width; p.silu = silu ? 1 : 0;
+  p.x = x; p.ldx = ldx; p.w = w; p.bias = bias;
+  p.state = state;
+  p.y = {{(int)dim0, (int)dim1, (int)dim2}, {y0, y1, y2}};
+  const int64_t v = 16 / (int64_t)es;
+  const bool vec = vec_rows(x, ldx, es) && dim0 % v == 0 && dim1 % v == 0 && dim2 % v == 0 && vec_rows(y0, 0, es) &&
+                   vec_rows(y1, 0, es) && vec_rows(y2, 0, es);
+  if (launch_injected())
+    return fail(SS_ERR_CUDA, "%s: launch failure injected by SS_FAIL_LAUNCH (nothing enqueued)", fn);
+  cudaError_t e = ss::launch_conv_tm_fwd(p, static_cast<ss::DType>(dtype), vec, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(SS_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return SS_OK;
+}
+
+size_t ss_conv1d_tm_bwd_workspace_size(int64_t tokens, int64_t dim, int64_t width) {
+  ss::Ragged r;
+  if (check_conv_tm("ss_conv1d_tm_bwd_workspace_size", dim, width, SS_F32, dim, 0, 0) != SS_OK ||
+      check_ragged("ss_conv1d_tm_bwd_workspace_size", tokens, 1, nullptr, false, 0, nullptr, &r, nullptr) != SS_OK)
+    return (size_t)-1;
+  int strip = 0, nstrip = 0;
+  conv_tm_strips(tokens, &strip, &nstrip);
+  return round_up((size_t)nstrip * dim * (width + 1) * sizeof(float), 256);
+}
+
+ss_status ss_conv1d_tm_bwd(int64_t tokens, int64_t nseq, int64_t dim, int64_t width, int dtype, const void* x,
+                           int64_t ldx, const float* w, const float* bias, const int32_t* cu_seqlens, int silu,
+                           int64_t dim0, int64_t dim1, int64_t dim2, const void* dy0, const void* dy1,
+                           const void* dy2, void* dx, int64_t lddx, float* dw, float* dbias, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const char* fn = "ss_conv1d_tm_bwd";
+  ss::ConvTmParams p{};
+  ss_status st = check_conv_tm(fn, dim, width, dtype, dim0, dim1, dim2);
+  if (st != SS_OK) return st;
+  if ((st = check_ragged(fn, tokens, nseq, cu_seqlens, false, 0, nullptr, &p.seq, &p.slots)) != SS_OK) return st;
+  const size_t es = elt_size(dtype);
+  if ((st = check_rows(fn, "x", x, ldx, dim, es, tokens)) != SS_OK) return st;
+  if ((st = check_rows(fn, "dx", dx, lddx, dim, es, tokens)) != SS_OK) return st;
+  if (!w || !dw || (tokens > 0 && (!dy0 || (dim1 && !dy1) || (dim2 && !dy2))))
+    return fail(SS_ERR_INVALID_ARG, "%s: w, dw and a gradient per piece are required", fn);
+  for (const void* q : {dy0, dy1, dy2})
+    if (q && !aligned(q, es)) return fail(SS_ERR_ALIGNMENT, "%s: gradient %p not aligned to %zu bytes", fn, q, es);
+  for (const void* q : {(const void*)w, (const void*)bias, (const void*)dw, (const void*)dbias})
+    if (q && !aligned(q, 4)) return fail(SS_ERR_ALIGNMENT, "%s: fp32 pointer %p not 4-byte aligned", fn, q);
+  conv_tm_strips(tokens, &p.strip, &p.nstrip);
+  const size_t need = round_up((size_t)p.nstrip * dim * (width + 1) * sizeof(float), 256);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(SS_ERR_WORKSPACE, "%s: needs %zu workspace bytes, got %zu", fn, need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (workspace && !aligned(workspace, 16)) return fail(SS_ERR_ALIGNMENT, "%s: workspace not 16-byte aligned", fn);
+  p.dim = (int)dim; p.width = (int)width; p.silu = silu ? 1 : 0;
+  p.x = x; p.ldx = ldx; p.w = w; p.bias = bias;
+  p.y = {{(int)dim0, (int)dim1, (int)dim2},
+         {const_cast<void*>(dy0), const_cast<void*>(dy1), const_cast<void*>(dy2)}};
+  p.dx = dx; p.lddx = lddx; p.dw = dw; p.dbias = dbias;
+  p.part = static_cast<float*>(workspace);
+  const bool vec = vec_rows(x, ldx, es) && vec_rows(dx, lddx, es) && dim0 % 4 == 0 && dim1 % 4 == 0 && dim2 % 4 == 0 &&
+                   vec_rows(dy0, 0, es) && vec_rows(dy1, 0, es) && vec_rows(dy2, 0, es);
+  if (launch_injected())
+    return fail(SS_ERR_CUDA, "%s: launch failure injected by SS_FAIL_LAUNCH (nothing enqueued)", fn);
+  cudaError_t e = ss::launch_conv_tm_bwd(p, static_cast<ss::DType>(dtype), vec, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(SS_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return SS_OK;
+}
+
+ss_status ss_gated_norm_fwd(int64_t rows, int64_t dim, int64_t group, int dtype, const void* x, int64_t ldx,
+                            const void* z, int64_t ldz, const float* w, float eps, int gate_last, void* y,
+                            float* rstd, void* stream) {
+  const char* fn = "ss_gated_norm_fwd";
+  ss_status st = check_norm(fn, rows, dim, group);
+  if (st != SS_OK) return st;
+  if ((st = check_dtype(dtype)) != SS_OK) return st;
+  const size_t es = elt_size(dtype);
+  if ((st = check_rows(fn, "x", x, ldx, dim, es, rows)) != SS_OK) return st;
+  if (z && (st = check_rows(fn, "z", z, ldz, dim, es, rows)) != SS_OK) return st;
+  if (!w || (rows > 0 && !y)) return fail(SS_ERR_INVALID_ARG, "%s: w and y are required", fn);
+  if (!(eps >= 0.f)) return fail(SS_ERR_INVALID_ARG, "%s: eps must not be negative", fn);
+  if (y && !aligned(y, es)) return fail(SS_ERR_ALIGNMENT, "%s: y not aligned to %zu bytes", fn, es);
+  for (const void* q : {(const void*)w, (const void*)rstd})
+    if (q && !aligned(q, 4)) return fail(SS_ERR_ALIGNMENT, "%s: fp32 pointer %p not 4-byte aligned", fn, q);
+  if (rows == 0) return SS_OK;
+  ss::NormParams p{};
+  p.rows = rows; p.dim = (int)dim; p.group = (int)group; p.gate_last = gate_last ? 1 : 0;
+  p.x = x; p.ldx = ldx; p.z = z; p.ldz = ldz; p.w = w; p.eps = eps; p.y = y; p.rstd = rstd;
+  const bool vec = group % 8 == 0 && vec_rows(x, ldx, es) && vec_rows(z, ldz, es) && vec_rows(y, dim, es) &&
+                   aligned(w, 16);
+  if (launch_injected())
+    return fail(SS_ERR_CUDA, "%s: launch failure injected by SS_FAIL_LAUNCH (nothing enqueued)", fn);
+  cudaError_t e = ss::launch_gated_norm(p, false, static_cast<ss::DType>(dtype), vec, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(SS_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return SS_OK;
+}
+
+size_t ss_gated_norm_bwd_workspace_size(int64_t rows, int64_t dim, int64_t group) {
+  if (check_norm("ss_gated_norm_bwd_workspace_size", rows, dim, group) != SS_OK) return (size_t)-1;
+  size_t parts = 0;
+  for (bool vec : {false, true}) {  // either layout of the rows
+    if (vec && group % 8) continue;
+    const int slots = ss::norm_slots((int)group, vec);
+    const size_t n = (size_t)norm_blocks(rows, dim, group, slots) * slots;
+    if (n > parts) parts = n;
+  }
+  return round_up(parts * dim * sizeof(float), 256);
+}
+
+ss_status ss_gated_norm_bwd(int64_t rows, int64_t dim, int64_t group, int dtype, const void* x, int64_t ldx,
+                            const void* z, int64_t ldz, const float* w, const float* rstd, const void* dy,
+                            int gate_last, void* dx, int64_t lddx, void* dz, int64_t lddz, float* dw,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "ss_gated_norm_bwd";
+  ss_status st = check_norm(fn, rows, dim, group);
+  if (st != SS_OK) return st;
+  if ((st = check_dtype(dtype)) != SS_OK) return st;
+  const size_t es = elt_size(dtype);
+  if ((st = check_rows(fn, "x", x, ldx, dim, es, rows)) != SS_OK) return st;
+  if ((st = check_rows(fn, "dx", dx, lddx, dim, es, rows)) != SS_OK) return st;
+  if (z && (st = check_rows(fn, "z", z, ldz, dim, es, rows)) != SS_OK) return st;
+  if (z && (st = check_rows(fn, "dz", dz, lddz, dim, es, rows)) != SS_OK) return st;
+  if (dz && !z) return fail(SS_ERR_INVALID_ARG, "%s: dz given without z", fn);
+  if (!w || !dw || (rows > 0 && (!rstd || !dy)))
+    return fail(SS_ERR_INVALID_ARG, "%s: w, rstd, dy and dw are required", fn);
+  if (dy && !aligned(dy, es)) return fail(SS_ERR_ALIGNMENT, "%s: dy not aligned to %zu bytes", fn, es);
+  for (const void* q : {(const void*)w, (const void*)rstd, (const void*)dw})
+    if (q && !aligned(q, 4)) return fail(SS_ERR_ALIGNMENT, "%s: fp32 pointer %p not 4-byte aligned", fn, q);
+  const size_t need = ss_gated_norm_bwd_workspace_size(rows, dim, group);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(SS_ERR_WORKSPACE, "%s: needs %zu workspace bytes, got %zu", fn, need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (workspace && !aligned(workspace, 16)) return fail(SS_ERR_ALIGNMENT, "%s: workspace not 16-byte aligned", fn);
+  ss::NormParams p{};
+  p.rows = rows; p.dim = (int)dim; p.group = (int)group; p.gate_last = gate_last ? 1 : 0;
+  p.x = x; p.ldx = ldx; p.z = z; p.ldz = ldz; p.w = w; p.rstd = const_cast<float*>(rstd); p.dy = dy;
+  p.dx = dx; p.lddx = lddx; p.dz = dz; p.lddz = lddz; p.dw = dw; p.part = static_cast<float*>(workspace);
+  const bool vec = group % 8 == 0 && vec_rows(x, ldx, es) && vec_rows(z, ldz, es) && vec_rows(dy, dim, es) &&
+                   vec_rows(dx, lddx, es) && vec_rows(dz, lddz, es) && aligned(w, 16);
+  p.nblk = norm_blocks(rows, dim, group, ss::norm_slots((int)group, vec));
+  if (launch_injected())
+    return fail(SS_ERR_CUDA, "%s: launch failure injected by SS_FAIL_LAUNCH (nothing enqueued)", fn);
+  cudaError_t e = ss::launch_gated_norm(p, true, static_cast<ss::DType>(dtype), vec, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(SS_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return SS_OK;
+}
+
+static ss_status check_heads(const char* fn, int64_t nheads, int64_t headdim, int64_t ngroups, int64_t dstate) {
+  if (nheads <= 0 || ngroups <= 0 || nheads % ngroups)
+    return fail(SS_ERR_INVALID_ARG, "%s: ngroups=%lld must divide nheads=%lld", fn, (long long)ngroups,
+                (long long)nheads);
+  if (headdim != 64 || (dstate != 64 && dstate != 128))
+    return fail(SS_ERR_UNSUPPORTED, "%s: headdim=%lld dstate=%lld (supported: headdim 64, dstate 64 or 128)", fn,
+                (long long)headdim, (long long)dstate);
+  if (nheads > 8192) return fail(SS_ERR_UNSUPPORTED, "%s: nheads above 8192", fn);
+  return SS_OK;
+}
+
+size_t ss_ssd_step_workspace_size(int64_t batch, int64_t nheads, int64_t headdim, int64_t ngroups, int64_t dstate) {
+  if (check_heads("ss_ssd_step_workspace_size", nheads, headdim, ngroups, dstate) != SS_OK) return (size_t)-1;
+  if (batch < 0 || batch > 65535) {
+    fail(SS_ERR_UNSUPPORTED, "ss_ssd_step_workspace_size: batch=%lld (supported: 0..65535)", (long long)batch);
+    return (size_t)-1;
+  }
+  return round_up((size_t)batch * (nheads * headdim + 2 * ngroups * dstate) * sizeof(float), 256);
+}
+
+ss_status ss_ssd_step(int64_t batch, int64_t nheads, int64_t headdim, int64_t ngroups, int64_t dstate, int64_t width,
+                      int dtype, const void* xbc, int64_t ldx, const void* dt, int64_t lddt, const float* w,
+                      const float* conv_bias, int silu, const float* A, const float* D, const void* z, int64_t ldz,
+                      const float* dt_bias, int dt_softplus, float* conv_state, float* state, int64_t nslots,
+                      const int32_t* slots, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "ss_ssd_step";
+  ss_status st = check_heads(fn, nheads, headdim, ngroups, dstate);
+  if (st != SS_OK) return st;
+  if ((st = check_dtype(dtype)) != SS_OK) return st;
+  if (width < 1 || width > 4)
+    return fail(SS_ERR_UNSUPPORTED, "%s: width=%lld (supported: 1..4)", fn, (long long)width);
+  if (batch < 0 || batch > 65535)
+    return fail(SS_ERR_UNSUPPORTED, "%s: batch=%lld (supported: 0..65535)", fn, (long long)batch);
+  ss::SsdStepParams p{};
+  ss::Ragged r;
+  if ((st = check_ragged(fn, batch, batch, nullptr, true, nslots, slots, &r, &p.slots)) != SS_OK) return st;
+  const size_t es = elt_size(dtype);
+  const int64_t d = nheads * headdim, dim = d + 2 * ngroups * dstate;
+  if ((st = check_rows(fn, "xbc", xbc, ldx, dim, es, batch)) != SS_OK) return st;
+  if ((st = check_rows(fn, "dt", dt, lddt, nheads, es, batch)) != SS_OK) return st;
+  if (z && (st = check_rows(fn, "z", z, ldz, d, es, batch)) != SS_OK) return st;
+  if (!w || !A || !state || (!conv_state && width > 1) || (batch > 0 && !y))
+    return fail(SS_ERR_INVALID_ARG, "%s: w, A, conv_state, state and y are required", fn);
+  if (y && !aligned(y, es)) return fail(SS_ERR_ALIGNMENT, "%s: y not aligned to %zu bytes", fn, es);
+  for (const void* q : {(const void*)w, (const void*)conv_bias, (const void*)A, (const void*)D, (const void*)dt_bias,
+                        (const void*)conv_state})
+    if (q && !aligned(q, 4)) return fail(SS_ERR_ALIGNMENT, "%s: fp32 pointer %p not 4-byte aligned", fn, q);
+  if (!aligned(state, 16)) return fail(SS_ERR_ALIGNMENT, "%s: state not 16-byte aligned", fn);
+  const size_t need = round_up((size_t)batch * dim * sizeof(float), 256);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(SS_ERR_WORKSPACE, "%s: needs %zu workspace bytes, got %zu", fn, need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (workspace && !aligned(workspace, 16)) return fail(SS_ERR_ALIGNMENT, "%s: workspace not 16-byte aligned", fn);
+  if (batch == 0) return SS_OK;
+  p.batch = (int)batch; p.nheads = (int)nheads; p.headdim = (int)headdim; p.ngroups = (int)ngroups;
+  p.dstate = (int)dstate; p.width = (int)width; p.silu = silu ? 1 : 0; p.softplus = dt_softplus ? 1 : 0;
+  p.xbc = xbc; p.ldx = ldx; p.dt = dt; p.lddt = lddt; p.z = z; p.ldz = ldz;
+  p.w = w; p.bias = conv_bias; p.A = A; p.D = D; p.dt_bias = dt_bias;
+  p.conv_state = conv_state; p.state = state; p.y = y; p.xconv = static_cast<float*>(workspace);
+  if (launch_injected())
+    return fail(SS_ERR_CUDA, "%s: launch failure injected by SS_FAIL_LAUNCH (nothing enqueued)", fn);
+  cudaError_t e = ss::launch_ssd_step(p, static_cast<ss::DType>(dtype), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(SS_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+  return SS_OK;
+}
+
+size_t ss_ssd_prefill_workspace_size(int64_t tokens, int64_t nseq, int64_t nheads, int64_t headdim, int64_t ngroups,
+                                     int64_t dstate) {
+  ss::Ragged r;
+  static const int32_t any = 0;
+  if (check_heads("ss_ssd_prefill_workspace_size", nheads, headdim, ngroups, dstate) != SS_OK ||
+      check_ragged("ss_ssd_prefill_workspace_size", tokens, nseq, &any, false, 0, nullptr, &r, nullptr) != SS_OK)
+    return (size_t)-1;
+  return 0;
+}
+
+ss_status ss_ssd_prefill(int64_t tokens, int64_t nseq, int64_t nheads, int64_t headdim, int64_t ngroups,
+                         int64_t dstate, int dtype, const void* x, int64_t ldx, const void* dt, int64_t lddt,
+                         const float* A, const void* B, int64_t ldb, const void* C, int64_t ldc, const float* D,
+                         const void* z, int64_t ldz, const float* dt_bias, int dt_softplus,
+                         const int32_t* cu_seqlens, float* state, int64_t nslots, const int32_t* slots,
+                         const uint8_t* fresh, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "ss_ssd_prefill";
+  ss_status st = check_heads(fn, nheads, headdim, ngroups, dstate);
+  if (st != SS_OK) return st;
+  if (dtype != SS_BF16 && dtype != SS_F16)
+    return fail(SS_ERR_UNSUPPORTED, "%s: dtype %d (supported: bf16, fp16 storage)", fn, dtype);
+  ss::SsdPrefillParams p{};
+  if ((st = check_ragged(fn, tokens, nseq, cu_seqlens, state != nullptr, nslots, slots, &p.seq, &p.slots)) != SS_OK)
+    return st;
+  const size_t es = elt_size(dtype);
+  const int64_t d = nheads * headdim, gn = ngroups * dstate;
+  if ((st = check_rows(fn, "x", x, ldx, d, es, tokens)) != SS_OK) return st;
+  if ((st = check_rows(fn, "dt", dt, lddt, nheads, es, tokens)) != SS_OK) return st;
+  if ((st = check_rows(fn, "B", B, ldb, gn, es, tokens)) != SS_OK) return st;
+  if ((st = check_rows(fn, "C", C, ldc, gn, es, tokens)) != SS_OK) return st;
+  if (z && (st = check_rows(fn, "z", z, ldz, d, es, tokens)) != SS_OK) return st;
+  if (!A || (tokens > 0 && !y)) return fail(SS_ERR_INVALID_ARG, "%s: A and y are required", fn);
+  // x, B and C are operand tiles of the tensor cores: their rows start on 16-byte boundaries
+  for (auto q : {std::make_pair(x, ldx), std::make_pair(B, ldb), std::make_pair(C, ldc)})
+    if (!vec_rows(q.first, q.second, es))
+      return fail(SS_ERR_ALIGNMENT, "%s: rows of x, B and C must start on 16-byte boundaries", fn);
+  if (y && !aligned(y, 16)) return fail(SS_ERR_ALIGNMENT, "%s: y not 16-byte aligned", fn);
+  for (const void* q : {(const void*)A, (const void*)D, (const void*)dt_bias})
+    if (q && !aligned(q, 4)) return fail(SS_ERR_ALIGNMENT, "%s: fp32 pointer %p not 4-byte aligned", fn, q);
+  if (state && !aligned(state, 16)) return fail(SS_ERR_ALIGNMENT, "%s: state not 16-byte aligned", fn);
+  const size_t need = ss_ssd_prefill_workspace_size(tokens, nseq, nheads, headdim, ngroups, dstate);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(SS_ERR_WORKSPACE, "%s: needs %zu workspace bytes, got %zu", fn, need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (workspace && !aligned(workspace, 256)) return fail(SS_ERR_ALIGNMENT, "%s: workspace not 256-byte aligned", fn);
+  if (nseq == 0) return SS_OK;
+  if (current_sm_count(&p.sms) != 0) return fail(SS_ERR_CUDA, "%s: cannot query the device", fn);
+  p.slots.fresh = fresh;
+  p.nheads = (int)nheads; p.headdim = (int)headdim; p.ngroups = (int)ngroups; p.dstate = (int)dstate;
+  p.softplus = dt_softplus ? 1 : 0;
+  p.x = x; p.ldx = ldx; p.dt = dt; p.lddt = lddt; p.B = B; p.ldb = ldb; p.C = C; p.ldc = ldc; p.z = z; p.ldz = ldz;
+  p.A = A; p.D = D; p.dt_bias = dt_bias; p.state = state; p.y = y; p.ws = workspace;
+  if (launch_injected())
+    return fail(SS_ERR_CUDA, "%s: launch failure injected by SS_FAIL_LAUNCH (nothing enqueued)", fn);
+  cudaError_t e = ss::launch_ssd_prefill(p, static_cast<ss::DType>(dtype), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(SS_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return SS_OK;
 }
 

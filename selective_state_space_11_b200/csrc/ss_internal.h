@@ -166,4 +166,95 @@ cudaError_t plan_bwd_ch(BwdParams& p, DType dt);
 cudaError_t launch_bwd_ch(const BwdParams& p, DType dt, cudaStream_t s);
 cudaError_t launch_state_update(const UpdateParams& p, DType dt, cudaStream_t s);
 
+// ---- time-major (Mamba-2) operators around the SSD scan -------------------
+// Sequences packed along the token axis: sequence i holds the tokens
+// [cu[i], cu[i + 1]), or without cu seqlen tokens each.
+struct Ragged {
+  const int* cu;              // (nseq + 1,) or null
+  int nseq, tokens, seqlen;
+};
+// A state cache of `count` slots; sequence i uses slot index[i] (slot i without index).
+struct Slots {
+  const int* index;           // (nseq,) or null
+  const unsigned char* fresh; // (nseq,): nonzero starts from a zero state; null: none does
+  int count;
+};
+// The column pieces a packed row is split into: widths (their sum is the row) and base pointers.
+struct Pieces {
+  int width[3];
+  void* p[3];
+};
+
+struct ConvTmParams {
+  Ragged seq;
+  Slots slots;
+  int dim, width, silu;
+  const void* x;              // (tokens, dim), rows ldx apart
+  int64_t ldx;
+  const float *w, *bias;      // (dim, width), (dim,) or null
+  float* state;               // (slots, dim, width-1) in/out, or null
+  Pieces y;                   // forward: outputs; backward: their gradients
+  void* dx;                   // backward: (tokens, dim), rows lddx apart
+  int64_t lddx;
+  float *dw, *dbias;          // backward; dbias may be null
+  float* part;                // backward workspace: (strips, dim, width + 1)
+  int strip, nstrip;          // backward: tokens per strip, strips
+};
+
+struct NormParams {
+  int64_t rows;
+  int dim, group, gate_last;  // gate_last: the gate multiplies the normalised row
+  const void *x, *z;          // rows ldx, ldz apart; z may be null (no gate)
+  int64_t ldx, ldz;
+  const float* w;             // (dim,)
+  float eps;
+  void* y;                    // (rows, dim)
+  float* rstd;                // (rows, dim / group): written by the forward (or null), read by the backward
+  const void* dy;             // backward: (rows, dim)
+  void *dx, *dz;              // rows lddx, lddz apart; dz null without z
+  int64_t lddx, lddz;
+  float* dw;                  // (dim,)
+  float* part;                // backward workspace: (parts, dim)
+  int nblk;                   // backward: blocks per group
+};
+
+struct SsdStepParams {
+  Slots slots;
+  int batch, nheads, headdim, ngroups, dstate, width, silu, softplus;
+  const void *xbc, *dt, *z;   // (batch, conv dim), (batch, nheads), (batch, nheads * headdim) or null
+  int64_t ldx, lddt, ldz;
+  const float *w, *bias;      // (conv dim, width), (conv dim,) or null
+  const float *A, *D, *dt_bias;
+  float* conv_state;          // (slots, conv dim, width - 1) in/out
+  float* state;               // (slots, nheads, headdim, dstate) in/out
+  void* y;                    // (batch, nheads, headdim)
+  float* xconv;               // workspace (batch, conv dim): the convolution's outputs
+};
+
+struct SsdPrefillParams {
+  Ragged seq;
+  Slots slots;
+  int nheads, headdim, ngroups, dstate, softplus;
+  const void *x, *dt, *B, *C, *z;  // (tokens, ...) rows ldx, lddt, ldb, ldc, ldz apart; z may be null
+  int64_t ldx, lddt, ldb, ldc, ldz;
+  const float *A, *D, *dt_bias;
+  float* state;               // (slots, nheads, headdim, dstate) in/out, or null
+  void* y;                    // (tokens, nheads, headdim)
+  void* ws;
+  int sms;
+};
+
+cudaError_t launch_conv_tm_fwd(const ConvTmParams& p, DType dt, bool vec, int sms, cudaStream_t s);
+cudaError_t launch_conv_tm_bwd(const ConvTmParams& p, DType dt, bool vec, cudaStream_t s);
+// Column groups (of `group` columns, 16-byte vectors or not) that a block of the norm holds at once.
+int norm_slots(int group, bool vec);
+constexpr int kMaxNormGroup = 8192;
+cudaError_t launch_gated_norm(const NormParams& p, bool backward, DType dt, bool vec, cudaStream_t s);
+cudaError_t launch_ssd_step(const SsdStepParams& p, DType dt, cudaStream_t s);
+cudaError_t launch_ssd_prefill(const SsdPrefillParams& p, DType dt, cudaStream_t s);
+// Their fault words (an index out of range or used twice: bit 3; waits: bits 0..2).
+cudaError_t read_fault_conv_tm(unsigned* bits, bool clear);
+cudaError_t read_fault_step(unsigned* bits, bool clear);
+cudaError_t read_fault_prefill(unsigned* bits, bool clear);
+
 }  // namespace ss

@@ -62,6 +62,21 @@ SIGNATURES = {
     "ss_ssd_bwd_workspace_size": ([_I64, _I64, _I64, _I64, _I64, _I64], _SZ),
     "ss_ssd_bwd": ([_I64, _I64, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P,
                     _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "ss_conv1d_tm_fwd": ([_I64, _I64, _I64, _I64, _I, _P, _I64, _P, _P, _P, _P, _I64, _P, _P, _I, _I64, _I64,
+                          _I64, _P, _P, _P, _P], _I),
+    "ss_conv1d_tm_bwd_workspace_size": ([_I64, _I64, _I64], _SZ),
+    "ss_conv1d_tm_bwd": ([_I64, _I64, _I64, _I64, _I, _P, _I64, _P, _P, _P, _I, _I64, _I64, _I64, _P, _P, _P,
+                          _P, _I64, _P, _P, _P, _SZ, _P], _I),
+    "ss_ssd_prefill_workspace_size": ([_I64, _I64, _I64, _I64, _I64, _I64], _SZ),
+    "ss_ssd_prefill": ([_I64, _I64, _I64, _I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P, _P, _I64, _P, _I64, _P,
+                        _P, _I64, _P, _I, _P, _P, _I64, _P, _P, _P, _P, _SZ, _P], _I),
+    "ss_ssd_step_workspace_size": ([_I64, _I64, _I64, _I64, _I64], _SZ),
+    "ss_ssd_step": ([_I64, _I64, _I64, _I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P, _P, _I, _P, _P, _P, _I64,
+                     _P, _I, _P, _P, _I64, _P, _P, _P, _SZ, _P], _I),
+    "ss_gated_norm_fwd": ([_I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P, ctypes.c_float, _I, _P, _P, _P], _I),
+    "ss_gated_norm_bwd_workspace_size": ([_I64, _I64, _I64], _SZ),
+    "ss_gated_norm_bwd": ([_I64, _I64, _I64, _I, _P, _I64, _P, _I64, _P, _P, _P, _I, _P, _I64, _P, _I64, _P, _P,
+                           _SZ, _P], _I),
     "ss_state_update": ([_I64, _I64, _I64, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P],
                         _I),
 }
@@ -522,6 +537,340 @@ def ssd_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_softplus=True, 
                                 _ptr(g["dC"]), _ptr(g["dD"]), _ptr(g["dz"]), _ptr(g["ddt_bias"]),
                                 _ptr(g["dh0"]), _ptr(workspace), int(workspace.numel()), _stream(dev)))
     return g
+
+
+# ---- time-major operators around the SSD scan (Mamba-2) ---------------------
+def _need_rows(t: torch.Tensor, name: str, lead, tail, dtype, dev) -> int:
+    """Check a tensor of shape lead + tail whose rows (the tail) are contiguous and
+    evenly spaced along the lead axes; returns the distance between rows in elements."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if tuple(t.shape) != tuple(lead) + tuple(tail):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(lead) + tuple(tail)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    width = 1
+    for size, stride in zip(reversed(tail), reversed(t.stride()[len(lead):])):
+        if size != 1 and stride != width:
+            raise ValueError(f"{name}: the elements of a row must be contiguous (strides {t.stride()})")
+        width *= size
+    ld, rows = width, 1
+    for k, (size, stride) in enumerate(zip(reversed(lead), reversed(t.stride()[:len(lead)]))):
+        if size == 1 or t.numel() == 0:
+            pass
+        elif rows == 1:
+            if stride < width:
+                raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+            ld = stride
+        elif stride != ld * rows:
+            raise ValueError(f"{name}: rows must be evenly spaced (strides {t.stride()})")
+        rows *= size
+    return ld
+
+
+def _ragged(lead, cu_seqlens, dev) -> Tuple[int, int]:
+    """(tokens, sequences) of a token axis: (batch, L) rows, or (tokens,) with cu_seqlens."""
+    if len(lead) == 2:
+        if cu_seqlens is not None:
+            raise ValueError("cu_seqlens goes with a flat token axis, not with (batch, L)")
+        return lead[0] * lead[1], lead[0]
+    if len(lead) != 1:
+        raise ValueError(f"the token axes are (tokens,) or (batch, L), got {tuple(lead)}")
+    if cu_seqlens is None:
+        return lead[0], 1
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens has one offset per sequence and the end")
+    _need(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, dev)
+    return lead[0], cu_seqlens.numel() - 1
+
+
+def _slot_args(nseq, slots, fresh, dev):
+    _need(slots, "slots", (nseq,), torch.int32, dev, optional=True)
+    if fresh is not None and fresh.dtype == torch.bool:
+        fresh = fresh.view(torch.uint8)
+    _need(fresh, "fresh", (nseq,), torch.uint8, dev, optional=True)
+    return fresh
+
+
+def _ws(need: int, workspace, dev):
+    """The caller's workspace when it is large enough, else a new one (None when none is needed)."""
+    if need == ctypes.c_size_t(-1).value:
+        raise SSError(1, lib().ss_last_error().decode())
+    if need == 0:
+        return None
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        return torch.empty(need, device=dev, dtype=torch.uint8)
+    _need(workspace, "workspace", workspace.shape, workspace.dtype, dev)
+    return workspace
+
+
+def _check_conv_tm(x, w, bias, splits, cu_seqlens):
+    if x.dtype not in _DTYPE:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x is (tokens, dim) or (batch, L, dim), got {tuple(x.shape)}")
+    dev, lead, dim, W = x.device, tuple(x.shape[:-1]), x.shape[-1], w.shape[-1]
+    ldx = _need_rows(x, "x", lead, (dim,), x.dtype, dev)
+    tokens, nseq = _ragged(lead, cu_seqlens, dev)
+    _need(w, "w", (dim, W), torch.float32, dev)
+    _need(bias, "bias", (dim,), torch.float32, dev, optional=True)
+    splits = (dim,) if splits is None else tuple(int(s) for s in splits)
+    if not 1 <= len(splits) <= 3 or sum(splits) != dim or min(splits) <= 0:
+        raise ValueError(f"splits {splits}: one to three positive widths that sum to {dim}")
+    return dev, lead, tokens, nseq, dim, W, ldx, splits
+
+
+def conv1d_tm_fwd(x, w, bias=None, splits=None, cu_seqlens=None, state=None, slots=None, fresh=None, silu=True,
+                  out=None) -> Tuple[torch.Tensor, ...]:
+    """Time-major causal depthwise conv1d (+ SiLU) of packed rows, split into pieces.
+
+    x: (tokens, dim) or (batch, L, dim), rows may be a column slice of a wider
+    tensor; w: (dim, W) fp32, W <= 4; bias: (dim,) fp32.  Returns one contiguous
+    tensor per width in ``splits`` (default: one piece).  cu_seqlens: (nseq + 1,)
+    int32 offsets of the sequences along a flat token axis (default: one sequence,
+    or one per batch row); rows of no sequence are not written.  state: (nslots,
+    dim, W-1) fp32 windows, updated in place; slots: (nseq,) int32 slot of each
+    sequence (default: its own number; negative: padding, skipped); fresh: (nseq,)
+    bool, True starts from zero instead of the slot's window.  ``out`` may supply the pieces.
+    """
+    dev, lead, tokens, nseq, dim, W, ldx, splits = _check_conv_tm(x, w, bias, splits, cu_seqlens)
+    nslots = 0
+    if state is not None:
+        nslots = state.shape[0]
+        _need(state, "state", (nslots, dim, W - 1), torch.float32, dev)
+    elif slots is not None or fresh is not None:
+        raise ValueError("slots and fresh go with a state cache")
+    fresh = _slot_args(nseq, slots, fresh, dev)
+    if out is None:
+        out = tuple(torch.empty(*lead, s, device=dev, dtype=x.dtype) for s in splits)
+    if len(out) != len(splits):
+        raise ValueError(f"out holds {len(out)} pieces, expected {len(splits)}")
+    for i, (o, s) in enumerate(zip(out, splits)):
+        _need(o, f"out[{i}]", lead + (s,), x.dtype, dev)
+    d = splits + (0,) * (3 - len(splits))
+    y = tuple(out) + (None,) * (3 - len(splits))
+    with torch.cuda.device(dev):
+        _check(lib().ss_conv1d_tm_fwd(tokens, nseq, dim, W, _DTYPE[x.dtype], _ptr(x), ldx, _ptr(w), _ptr(bias),
+                                      _ptr(cu_seqlens), _ptr(state), nslots, _ptr(slots), _ptr(fresh),
+                                      int(bool(silu)), *d, *map(_ptr, y), _stream(dev)))
+    return tuple(out)
+
+
+def conv1d_tm_bwd(x, w, dy, bias=None, cu_seqlens=None, silu=True, dx=None,
+                  workspace=None) -> Dict[str, Optional[torch.Tensor]]:
+    """Adjoint of conv1d_tm_fwd (without a cache) for sum_i <dy[i], y[i]>.
+
+    dy: the gradients of the pieces, contiguous.  Returns dx (like x; ``dx`` may
+    supply it, also as a column slice of a wider gradient; rows of no sequence
+    become zero), dw (dim, W) and dbias (dim,) fp32.
+    """
+    dev, lead, tokens, nseq, dim, W, ldx, splits = _check_conv_tm(x, w, bias, [t.shape[-1] for t in dy], cu_seqlens)
+    for i, (t, s) in enumerate(zip(dy, splits)):
+        _need(t, f"dy[{i}]", lead + (s,), x.dtype, dev)
+    if dx is None:
+        dx = torch.empty(*lead, dim, device=dev, dtype=x.dtype)
+    lddx = _need_rows(dx, "dx", lead, (dim,), x.dtype, dev)
+    f32 = dict(device=dev, dtype=torch.float32)
+    g = dict(dx=dx, dw=torch.empty(dim, W, **f32), dbias=torch.empty(dim, **f32))
+    d = splits + (0,) * (3 - len(splits))
+    t = tuple(dy) + (None,) * (3 - len(splits))
+    with torch.cuda.device(dev):
+        workspace = _ws(lib().ss_conv1d_tm_bwd_workspace_size(tokens, dim, W), workspace, dev)
+        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib().ss_conv1d_tm_bwd(tokens, nseq, dim, W, _DTYPE[x.dtype], _ptr(x), ldx, _ptr(w), _ptr(bias),
+                                      _ptr(cu_seqlens), int(bool(silu)), *d, *map(_ptr, t), _ptr(dx), lddx,
+                                      _ptr(g["dw"]), _ptr(g["dbias"]), _ptr(workspace), size, _stream(dev)))
+    return g
+
+
+class _CausalConv1dTm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, splits, cu_seqlens, silu):
+        y = conv1d_tm_fwd(x, w, bias, splits=splits, cu_seqlens=cu_seqlens, silu=silu)
+        ctx.save_for_backward(x, w, bias, cu_seqlens)
+        ctx.silu = silu
+        return y
+
+    @staticmethod
+    def backward(ctx, *dy):
+        x, w, bias, cu_seqlens = ctx.saved_tensors
+        g = conv1d_tm_bwd(x, w, [t.contiguous() for t in dy], bias=bias, cu_seqlens=cu_seqlens, silu=ctx.silu)
+        return g["dx"], g["dw"], g["dbias"] if bias is not None else None, None, None, None
+
+
+def causal_conv1d_tm_fn(x, w, bias=None, splits=None, cu_seqlens=None, silu=True):
+    """Differentiable conv1d_tm_fwd (no cache): a tuple of pieces; x (tokens, dim) or (batch, L, dim)."""
+    return _CausalConv1dTm.apply(x, w, bias, splits, cu_seqlens, silu)
+
+
+def ssd_prefill(x, dt, A, B, C, state=None, D=None, z=None, dt_bias=None, dt_softplus=True, cu_seqlens=None,
+                slots=None, fresh=None, out=None, workspace=None) -> torch.Tensor:
+    """Mamba-2 SSD scan of ragged prompts on a cache of states.  Returns y.
+
+    x, z: (tokens, nheads, 64) or (batch, L, nheads, 64) bf16/fp16; dt: (tokens,
+    nheads); B, C: (tokens, ngroups, dstate), dstate 64 or 128; rows may be column
+    slices of wider tensors (x, B and C on 16-byte boundaries); A, D, dt_bias:
+    (nheads,) fp32.  state: (nslots, nheads, 64, dstate) fp32, updated in place, or
+    None (every sequence from zero).  cu_seqlens, slots, fresh: as in conv1d_tm_fwd.
+    ``out`` may supply y; rows of no sequence are not written.
+    """
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"unsupported dtype {x.dtype} (bf16 or fp16)")
+    if x.dim() not in (3, 4) or B.dim() != x.dim():
+        raise ValueError(f"x is (tokens, nheads, 64) or (batch, L, nheads, 64), got {tuple(x.shape)}")
+    dev, lead, (nh, P), (ng, N) = x.device, tuple(x.shape[:-2]), x.shape[-2:], B.shape[-2:]
+    ldx = _need_rows(x, "x", lead, (nh, P), x.dtype, dev)
+    tokens, nseq = _ragged(lead, cu_seqlens, dev)
+    lddt = _need_rows(dt, "dt", lead, (nh,), x.dtype, dev)
+    ldb = _need_rows(B, "B", lead, (ng, N), x.dtype, dev)
+    ldc = _need_rows(C, "C", lead, (ng, N), x.dtype, dev)
+    ldz = 0 if z is None else _need_rows(z, "z", lead, (nh, P), x.dtype, dev)
+    _need(A, "A", (nh,), torch.float32, dev)
+    _need(D, "D", (nh,), torch.float32, dev, optional=True)
+    _need(dt_bias, "dt_bias", (nh,), torch.float32, dev, optional=True)
+    nslots = 0
+    if state is not None:
+        nslots = state.shape[0]
+        _need(state, "state", (nslots, nh, P, N), torch.float32, dev)
+    elif slots is not None or fresh is not None:
+        raise ValueError("slots and fresh go with a state cache")
+    fresh = _slot_args(nseq, slots, fresh, dev)
+    y = out if out is not None else torch.empty(*lead, nh, P, device=dev, dtype=x.dtype)
+    _need(y, "out", lead + (nh, P), x.dtype, dev)
+    with torch.cuda.device(dev):
+        workspace = _ws(lib().ss_ssd_prefill_workspace_size(tokens, nseq, nh, P, ng, N), workspace, dev)
+        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib().ss_ssd_prefill(tokens, nseq, nh, P, ng, N, _DTYPE[x.dtype], _ptr(x), ldx, _ptr(dt), lddt,
+                                    _ptr(A), _ptr(B), ldb, _ptr(C), ldc, _ptr(D), _ptr(z), ldz, _ptr(dt_bias),
+                                    int(bool(dt_softplus)), _ptr(cu_seqlens), _ptr(state), nslots, _ptr(slots),
+                                    _ptr(fresh), _ptr(y), _ptr(workspace), size, _stream(dev)))
+    return y
+
+
+def ssd_step(xbc, dt, w, A, conv_state, state, conv_bias=None, D=None, z=None, dt_bias=None, dt_softplus=True,
+             silu=True, slots=None, ngroups=1, out=None, workspace=None) -> torch.Tensor:
+    """One decode token of each request: convolution window and SSD state advance in
+    place.  Returns y (batch, nheads, 64).
+
+    xbc: (batch, nheads * 64 + 2 * ngroups * dstate) packed x|B|C, dt: (batch,
+    nheads), z: (batch, nheads * 64), rows may be column slices; w: (conv dim, W)
+    fp32; conv_state: (nslots, conv dim, W-1), state: (nslots, nheads, 64, dstate)
+    fp32; slots: (batch,) int32 (default: the request's own number; negative:
+    padding, whose row of y is not written).
+    """
+    if xbc.dtype not in _DTYPE:
+        raise ValueError(f"unsupported dtype {xbc.dtype}")
+    if state.dim() != 4 or xbc.dim() != 2:
+        raise ValueError("state is (nslots, nheads, 64, dstate), xbc (batch, conv dim)")
+    dev, bsz = xbc.device, xbc.shape[0]
+    nslots, nh, P, N = state.shape
+    dim, W = nh * P + 2 * ngroups * N, w.shape[-1]
+    ldx = _need_rows(xbc, "xbc", (bsz,), (dim,), xbc.dtype, dev)
+    lddt = _need_rows(dt, "dt", (bsz,), (nh,), xbc.dtype, dev)
+    ldz = 0 if z is None else _need_rows(z, "z", (bsz,), (nh * P,), xbc.dtype, dev)
+    _need(w, "w", (dim, W), torch.float32, dev)
+    _need(conv_bias, "conv_bias", (dim,), torch.float32, dev, optional=True)
+    _need(A, "A", (nh,), torch.float32, dev)
+    _need(D, "D", (nh,), torch.float32, dev, optional=True)
+    _need(dt_bias, "dt_bias", (nh,), torch.float32, dev, optional=True)
+    _need(conv_state, "conv_state", (nslots, dim, W - 1), torch.float32, dev)
+    _need(state, "state", (nslots, nh, P, N), torch.float32, dev)
+    _slot_args(bsz, slots, None, dev)
+    y = out if out is not None else torch.empty(bsz, nh, P, device=dev, dtype=xbc.dtype)
+    _need(y, "out", (bsz, nh, P), xbc.dtype, dev)
+    with torch.cuda.device(dev):
+        workspace = _ws(lib().ss_ssd_step_workspace_size(bsz, nh, P, ngroups, N), workspace, dev)
+        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib().ss_ssd_step(bsz, nh, P, ngroups, N, W, _DTYPE[xbc.dtype], _ptr(xbc), ldx, _ptr(dt), lddt,
+                                 _ptr(w), _ptr(conv_bias), int(bool(silu)), _ptr(A), _ptr(D), _ptr(z), ldz,
+                                 _ptr(dt_bias), int(bool(dt_softplus)), _ptr(conv_state), _ptr(state), nslots,
+                                 _ptr(slots), _ptr(y), _ptr(workspace), size, _stream(dev)))
+    return y
+
+
+def _check_norm(x, z, w, group):
+    if x.dtype not in _DTYPE:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x is (rows, dim) or (batch, L, dim), got {tuple(x.shape)}")
+    dev, lead, dim = x.device, tuple(x.shape[:-1]), x.shape[-1]
+    ldx = _need_rows(x, "x", lead, (dim,), x.dtype, dev)
+    ldz = 0 if z is None else _need_rows(z, "z", lead, (dim,), x.dtype, dev)
+    _need(w, "w", (dim,), torch.float32, dev)
+    group = dim if group is None else int(group)
+    if group <= 0 or dim % group:
+        raise ValueError(f"group={group} must divide dim={dim}")
+    rows = 1
+    for s in lead:
+        rows *= s
+    return dev, lead, rows, dim, group, ldx, ldz
+
+
+def gated_norm_fwd(x, z, w, group=None, eps=1e-5, gate_last=False, want_rstd=True, out=None):
+    """Gated RMS norm over groups of columns: y = rms(x silu(z)) w, or with
+    ``gate_last`` rms(x) w silu(z); z None: no gate.  Returns (y, rstd or None).
+
+    x, z: (rows, dim) or (batch, L, dim), rows may be column slices of wider
+    tensors; w: (dim,) fp32; group: columns normalised together (default: all; at
+    most 8192).  rstd (..., dim / group) fp32 is what gated_norm_bwd takes.
+    """
+    dev, lead, rows, dim, group, ldx, ldz = _check_norm(x, z, w, group)
+    y = out if out is not None else torch.empty(*lead, dim, device=dev, dtype=x.dtype)
+    _need(y, "out", lead + (dim,), x.dtype, dev)
+    rstd = torch.empty(*lead, dim // group, device=dev, dtype=torch.float32) if want_rstd else None
+    with torch.cuda.device(dev):
+        _check(lib().ss_gated_norm_fwd(rows, dim, group, _DTYPE[x.dtype], _ptr(x), ldx, _ptr(z), ldz, _ptr(w),
+                                       float(eps), int(bool(gate_last)), _ptr(y), _ptr(rstd), _stream(dev)))
+    return y, rstd
+
+
+def gated_norm_bwd(x, z, w, dy, rstd, group=None, gate_last=False, dx=None, dz=None,
+                   workspace=None) -> Dict[str, Optional[torch.Tensor]]:
+    """Adjoint of gated_norm_fwd for <dy, y>: dx, dz (None without z) in the input
+    dtype and dw (dim,) fp32.  ``dx`` and ``dz`` may be supplied, also as column
+    slices of a wider gradient."""
+    dev, lead, rows, dim, group, ldx, ldz = _check_norm(x, z, w, group)
+    _need(dy, "dy", lead + (dim,), x.dtype, dev)
+    _need(rstd, "rstd", lead + (dim // group,), torch.float32, dev)
+    if z is None and dz is not None:
+        raise ValueError("dz given without z")
+    new = dict(device=dev, dtype=x.dtype)
+    dx = torch.empty(*lead, dim, **new) if dx is None else dx
+    dz = torch.empty(*lead, dim, **new) if dz is None and z is not None else dz
+    lddx = _need_rows(dx, "dx", lead, (dim,), x.dtype, dev)
+    lddz = 0 if dz is None else _need_rows(dz, "dz", lead, (dim,), x.dtype, dev)
+    dw = torch.empty(dim, device=dev, dtype=torch.float32)
+    with torch.cuda.device(dev):
+        workspace = _ws(lib().ss_gated_norm_bwd_workspace_size(rows, dim, group), workspace, dev)
+        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib().ss_gated_norm_bwd(rows, dim, group, _DTYPE[x.dtype], _ptr(x), ldx, _ptr(z), ldz, _ptr(w),
+                                       _ptr(rstd), _ptr(dy), int(bool(gate_last)), _ptr(dx), lddx, _ptr(dz), lddz,
+                                       _ptr(dw), _ptr(workspace), size, _stream(dev)))
+    return dict(dx=dx, dz=dz, dw=dw)
+
+
+class _GatedNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, z, w, group, eps, gate_last):
+        y, rstd = gated_norm_fwd(x, z, w, group=group, eps=eps, gate_last=gate_last)
+        ctx.save_for_backward(x, z, w, rstd)
+        ctx.group, ctx.gate_last = group, gate_last
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, z, w, rstd = ctx.saved_tensors
+        g = gated_norm_bwd(x, z, w, dy.contiguous(), rstd, group=ctx.group, gate_last=ctx.gate_last)
+        return g["dx"], g["dz"], g["dw"], None, None, None
+
+
+def gated_norm_fn(x, z, w, group=None, eps=1e-5, gate_last=False):
+    """Differentiable gated_norm_fwd: returns y."""
+    return _GatedNorm.apply(x, z, w, group, eps, gate_last)
 
 
 class _SelectiveScan(torch.autograd.Function):
