@@ -472,7 +472,7 @@ SS_API ss_status ss_state_update(int64_t batch, int64_t dim, int64_t dstate, int
  *     calls capture into CUDA graphs, and a replay follows the data then in
  *     cu_seqlens, slots and fresh.
  *   - A NaN or an infinity in one sequence never reaches another's results.
- *   - Sizes: tokens < 2^31 - 2^16, nseq <= 2^20, batch <= 65535; tokens, nseq,
+ *   - Sizes: tokens < 2^31 - 2^16, nseq <= 65536, batch <= 65535; tokens, nseq,
  *     rows and batch may be 0.
  */
 
@@ -509,7 +509,8 @@ SS_API ss_status ss_conv1d_tm_bwd(int64_t tokens, int64_t nseq, int64_t dim, int
                                   int64_t lddx, float* dw, float* dbias, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
-/* Bytes of device workspace ss_ssd_prefill needs.  (size_t)-1 on invalid arguments. */
+/* Bytes of device workspace ss_ssd_prefill needs on the current device.
+ * (size_t)-1 on invalid arguments.  Calls that overlap need workspaces of their own. */
 SS_API size_t ss_ssd_prefill_workspace_size(int64_t tokens, int64_t nseq, int64_t nheads, int64_t headdim,
                                             int64_t ngroups, int64_t dstate);
 

@@ -796,8 +796,8 @@ constexpr int64_t kMaxTokens = INT32_MAX - 65536;  // tile and token arithmetic 
 ss_status check_ragged(const char* fn, int64_t tokens, int64_t nseq, const int32_t* cu_seqlens, bool cache,
                        int64_t nslots, const int32_t* slots, ss::Ragged* r, ss::Slots* c) {
   if (tokens < 0 || nseq < 0) return fail(SS_ERR_INVALID_ARG, "%s: tokens and nseq must not be negative", fn);
-  if (tokens > kMaxTokens || nseq > (1 << 20))
-    return fail(SS_ERR_UNSUPPORTED, "%s: sizes beyond the supported range (tokens < 2^31 - 2^16, nseq <= 2^20)", fn);
+  if (tokens > kMaxTokens || nseq > 65536)
+    return fail(SS_ERR_UNSUPPORTED, "%s: sizes beyond the supported range (tokens < 2^31 - 2^16, nseq <= 65536)", fn);
   if (!cu_seqlens && nseq > 0 && tokens % nseq)
     return fail(SS_ERR_INVALID_ARG, "%s: without cu_seqlens, nseq=%lld must divide tokens=%lld", fn, (long long)nseq,
                 (long long)tokens);
@@ -1112,7 +1112,12 @@ size_t ss_ssd_prefill_workspace_size(int64_t tokens, int64_t nseq, int64_t nhead
   if (check_heads("ss_ssd_prefill_workspace_size", nheads, headdim, ngroups, dstate) != SS_OK ||
       check_ragged("ss_ssd_prefill_workspace_size", tokens, nseq, &any, false, 0, nullptr, &r, nullptr) != SS_OK)
     return (size_t)-1;
-  return 0;
+  int sms = 0;
+  if (current_sm_count(&sms) != 0) {
+    fail(SS_ERR_CUDA, "cannot query the current device's SM count");
+    return (size_t)-1;
+  }
+  return ss::prefill_workspace(tokens, nseq, nheads, ngroups, dstate, sms);
 }
 
 ss_status ss_ssd_prefill(int64_t tokens, int64_t nseq, int64_t nheads, int64_t headdim, int64_t ngroups,
@@ -1145,13 +1150,13 @@ ss_status ss_ssd_prefill(int64_t tokens, int64_t nseq, int64_t nheads, int64_t h
   for (const void* q : {(const void*)A, (const void*)D, (const void*)dt_bias})
     if (q && !aligned(q, 4)) return fail(SS_ERR_ALIGNMENT, "%s: fp32 pointer %p not 4-byte aligned", fn, q);
   if (state && !aligned(state, 16)) return fail(SS_ERR_ALIGNMENT, "%s: state not 16-byte aligned", fn);
-  const size_t need = ss_ssd_prefill_workspace_size(tokens, nseq, nheads, headdim, ngroups, dstate);
+  if (nseq == 0) return SS_OK;
+  if (current_sm_count(&p.sms) != 0) return fail(SS_ERR_CUDA, "%s: cannot query the device", fn);
+  const size_t need = ss::prefill_workspace(tokens, nseq, nheads, ngroups, dstate, p.sms);
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(SS_ERR_WORKSPACE, "%s: needs %zu workspace bytes, got %zu", fn, need,
                 workspace ? workspace_bytes : (size_t)0);
   if (workspace && !aligned(workspace, 256)) return fail(SS_ERR_ALIGNMENT, "%s: workspace not 256-byte aligned", fn);
-  if (nseq == 0) return SS_OK;
-  if (current_sm_count(&p.sms) != 0) return fail(SS_ERR_CUDA, "%s: cannot query the device", fn);
   p.slots.fresh = fresh;
   p.nheads = (int)nheads; p.headdim = (int)headdim; p.ngroups = (int)ngroups; p.dstate = (int)dstate;
   p.softplus = dt_softplus ? 1 : 0;

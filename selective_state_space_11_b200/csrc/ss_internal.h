@@ -251,6 +251,9 @@ int norm_slots(int group, bool vec);
 constexpr int kMaxNormGroup = 8192;
 cudaError_t launch_gated_norm(const NormParams& p, bool backward, DType dt, bool vec, cudaStream_t s);
 cudaError_t launch_ssd_step(const SsdStepParams& p, DType dt, cudaStream_t s);
+// Persistent blocks of the prefill, and its workspace, on a device of `sms` SMs.
+int prefill_blocks(int64_t tokens, int64_t nseq, int npairs, int sms);
+size_t prefill_workspace(int64_t tokens, int64_t nseq, int64_t nheads, int64_t ngroups, int64_t dstate, int sms);
 cudaError_t launch_ssd_prefill(const SsdPrefillParams& p, DType dt, cudaStream_t s);
 // Their fault words (an index out of range or used twice: bit 3; waits: bits 0..2).
 cudaError_t read_fault_conv_tm(unsigned* bits, bool clear);

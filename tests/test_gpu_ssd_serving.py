@@ -77,6 +77,20 @@ def test_ragged_prompts_on_a_cache(dtype, nh, ng, N, strided, lens):
     assert (y[sum(lens):] == 7).all(), "rows behind the last sequence were written"
 
 
+@pytest.mark.parametrize("dtype,nh,N", [("bf16", 3, 128), ("f16", 2, 64)])
+def test_long_sequences_split_over_blocks(dtype, nh, N):
+    """Sequences that many blocks share: states handed over at the cuts, ranges inside one sequence."""
+    lens = [3001, 5, 0, 1500, 260]
+    g, q, kw = make(sum(lens), nh, 1, N, dtype, 67)
+    state = torch.randn(5, nh, 64, N, device=DEV, generator=g)
+    fresh = torch.tensor([0, 0, 1, 1, 0], dtype=torch.bool, device=DEV)
+    slots = torch.tensor([4, 0, 3, 1, 2], dtype=torch.int32, device=DEV)
+    q["dt"][::3] = -6.0  # long memories: the state that is handed over matters far behind the cut
+    r = ref.ssd(**q, **kw, cu=cu_of(lens), state=state, slots=slots, fresh=fresh)
+    y = ops.ssd_prefill(**q, **kw, cu_seqlens=cu_of(lens), state=state, slots=slots, fresh=fresh)
+    check(y, state, r, TYPES[dtype])
+
+
 def test_bare_call_dense_batch_and_flags():
     g, q, _ = make(2 * 90, 4, 2, 128, "bf16", 17)
     q4 = {k: v if k == "A" else v.reshape(2, 90, *v.shape[1:]) for k, v in q.items()}
