@@ -235,6 +235,7 @@ struct SsdPrefillParams {
   Ragged seq;
   Slots slots;
   int nheads, headdim, ngroups, dstate, softplus;
+  int zvec;                   // rows of z start on 16-byte boundaries
   const void *x, *dt, *B, *C, *z;  // (tokens, ...) rows ldx, lddt, ldb, ldc, ldz apart; z may be null
   int64_t ldx, lddt, ldb, ldc, ldz;
   const float *A, *D, *dt_bias;

@@ -67,7 +67,9 @@ namespace {
 
 constexpr int kP = 64;         // head dimension
 constexpr int kQ = 128;        // chunk length
-constexpr int kThreads = 256;
+constexpr int kCompute = 256;  // threads of the 8 compute warps
+constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr int kThreads = kCompute + 64;
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr uint32_t kFlagLimit = 1u << 22;  // polls of a predecessor's flag
 constexpr uint32_t kG = 0, kYc = 128, kM = 256, kS = 384;  // TMEM columns (Ym over G)
@@ -158,24 +160,56 @@ struct Lay {
   static constexpr int kTile = N * 256;               // 128 rows x N 16-bit
   static constexpr int kB = 0;                        // two of them
   static constexpr int kC = 2 * kTile;
-  static constexpr int kX = kC + kTile;               // 2 heads x 128 rows x 128 B
-  static constexpr int kW = kX + 32768;               // 3 pieces x 2 heads x 64 rows x 128 B
-  static constexpr int kH = kW + 49152;               // 128 rows x N 16-bit
-  static constexpr int kF = kH + kTile;               // float [2 heads][128]: 2^(to the end of the block) Delta
-  static constexpr int kPre = kF + 1024;              // float [2][128]: log2 decay from the block's start
-  static constexpr int kDl = kPre + 1024;             // float [2][128]: Delta
-  static constexpr int kTot = kDl + 1024;             // float [2][4]: log2 decay of each block of 32
-  static constexpr int kMax = kTot + 32;              // unsigned [2]: largest |x| of the chunk (fp16)
+  static constexpr int kX = kC + kTile;               // two of 2 heads x 128 rows x 128 B: x, then y in its place
+  static constexpr int kW = kX + 65536;               // 3 pieces x 2 heads x 32 rows x 128 B
+  static constexpr int kH = kW + 24576;               // 128 rows x N 16-bit
+  static constexpr int kArr = kH + kTile;             // two of Arrays
+  static constexpr int kMax = kArr + 2 * 3104;        // unsigned [2]: largest |x| Delta of the chunk (fp16)
   static constexpr int kBars = kMax + 16;             // mbarriers
-  static constexpr int kSlot = kBars + 80;
+  static constexpr int kSlot = kBars + 128;
   static constexpr int kBytes = kSlot + 16;
   static constexpr int kAlloc = kBytes + 1024;
 };
-enum : int { kBarB0 = 0, kBarB1 = 1, kBarC = 2, kBarX = 3, kBarG = 4, kBarYc = 5, kBarS0 = 6, kBarYm = 7, kBarS1 = 8,
-             kNumBars = 9 };
+struct Arrays {      // per head of the pair and token of the chunk
+  float f[2][kQ];    // 2^(log2 decay from the token to the end of its block of 32) Delta
+  float pre[2][kQ];  // log2 decay from the start of the block up to the token
+  float dl[2][kQ];   // Delta
+  float tot[2][4];   // log2 decay of each block
+};
+static_assert(sizeof(Arrays) == 3104, "Lay::kMax");
+
+// mbarriers: copies landed; products done; 8 warps' arrivals
+enum : int {
+  kBarB = 0,      // [2]
+  kBarX = 2,      // [2]
+  kBarC = 4,
+  kBarG = 5,      // G
+  kBarYc = 6,     // C H^T
+  kBarYm = 7,     // M X
+  kBarS = 8,      // a quarter of S has read its Xw: four phases a chunk
+  kBarSall = 9,   // all of S
+  kBarW = 10,     // a quarter of Xw is written: four phases a chunk
+  kBarM = 11,     // M is written
+  kBarH = 12,     // the state copy is written and the accumulators are read: the next chunk's products may start
+  kBarY = 13,     // y is in place of x
+  kNumBars = 14
+};
 
 __device__ __forceinline__ uint32_t swz(int r, int c) {
   return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+// Barrier of the compute warps; true everywhere if any thread's flag is set.
+__device__ __forceinline__ bool compute_sync_or(bool v) {
+  int r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 256, p;\n selp.b32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((int)v)
+      : "memory");
+  return r != 0;
 }
 
 template <typename T> struct Pk;
@@ -197,56 +231,61 @@ template <> struct Pk<__half> {
     return __half22float2(*reinterpret_cast<__half2*>(&w));
   }
 };
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float* f) {
+  return make_uint4(Pk<T>::pack(f[0], f[1]), Pk<T>::pack(f[2], f[3]), Pk<T>::pack(f[4], f[5]), Pk<T>::pack(f[6], f[7]));
+}
 
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const SsdPrefillParams p, int npairs, int blocks, const __grid_constant__ CUtensorMap map_x,
-                      const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_c) {
+                      const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_c,
+                      const __grid_constant__ CUtensorMap map_y) {
   using L = Lay<N>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t kId = tc::idesc_f16(kBf16, 128, 128, false, false);  // G, Yc
   constexpr uint32_t kIdS = tc::idesc_f16(kBf16, 128, N, true, true);
   constexpr uint32_t kIdYm = tc::idesc_f16(kBf16, 128, 64, false, true);
   constexpr int HN = N / 2;          // state columns per thread
-  constexpr int kMma = 0, kTma = 128;
 
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = tc::saddr(smem_raw);
   const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
   unsigned char* const sm = smem_raw + pad;
   const uint32_t sb = raw + pad;
-  float* const sF = reinterpret_cast<float*>(sm + L::kF);
-  float* const sPre = reinterpret_cast<float*>(sm + L::kPre);
-  float* const sDl = reinterpret_cast<float*>(sm + L::kDl);
-  float* const sTot = reinterpret_cast<float*>(sm + L::kTot);
+  Arrays* const arr = reinterpret_cast<Arrays*>(sm + L::kArr);
   unsigned* const sMax = reinterpret_cast<unsigned*>(sm + L::kMax);
   uint32_t* const sslot = reinterpret_cast<uint32_t*>(sm + L::kSlot);
   __shared__ unsigned s_block;
+  __shared__ int s_abort;
   auto bar = [&](int i) { return sb + L::kBars + 8u * static_cast<uint32_t>(i); };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wg = tid >> 7, row = tid & 127, blk = row >> 5;  // TMEM lane = row
-  const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-  const int hrow = row >> 6;       // the head (of the two) of state row `row`
+  // compute warps: TMEM lane = row; a warpgroup per head of the pair
+  const int hd = (warp >> 2) & 1, blk = warp & 3, row = 32 * blk + lane;
+  const uint32_t lane_base = static_cast<uint32_t>(32 * blk) << 16;
+  const int hrow = row >> 6;         // the head of state row `row`
 
-  if (tid == kMma) {
+  if (tid == 0) {
 #pragma unroll
-    for (int i = 0; i < kNumBars; ++i) tc::mbar_init(bar(i), 1);
+    for (int i = 0; i < kNumBars; ++i) tc::mbar_init(bar(i), i >= kBarW ? 8 : 1);
     tc::fence_mbar_init();
+    s_abort = 0;
   }
-  if (tid == kTma) {
+  if (tid == 32 * kTmaWarp) {
     tc::prefetch_map(&map_x);
     tc::prefetch_map(&map_b);
     tc::prefetch_map(&map_c);
+    tc::prefetch_map(&map_y);
   }
   if (warp == 0) tc::tmem_alloc(tc::saddr(sslot), 512);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = *sslot;
-  {  // the blocks of M above the diagonal stay zero
+  if (warp < 8) {  // the blocks of M above the diagonal stay zero
     const uint32_t zero[16] = {};
-    for (int j = blk + 1; j < 4; ++j) tc::st32x32b_x16(tmem + lane_base + kM + 64 * wg + 16 * j, zero);
+    for (int j = blk + 1; j < 4; ++j) tc::st32x32b_x16(tmem + lane_base + kM + 64 * hd + 16 * j, zero);
     tc::st_wait();
   }
   pdl_wait();  // the plan is written
@@ -261,7 +300,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int me = (int)s_block;
   const Cut A = cuts[me], E = cuts[me + 1];
 
-  // bookkeeping of armed barriers for the drain (copy thread: loads, MMA thread: products)
+  // A wait that runs out, or that another thread's has, makes `ok` false; the
+  // thread goes on to the next place where its role leaves the loop.
+  bool ok = true;
+  auto wait = [&](int i, uint32_t parity, unsigned bit) {
+    if (tc::wait(bar(i), parity & 1u, 1)) return;
+    for (uint32_t n = 0; ok && n < kWaitLimit; ++n) {
+      if (tc::wait(bar(i), parity & 1u, 1)) return;
+      if (*reinterpret_cast<volatile int*>(&s_abort)) ok = false;
+    }
+    if (ok) {
+      atomicOr(&g_fault_prefill, bit);
+      s_abort = 1;
+      ok = false;
+    }
+  };
+  // barriers that the copy and the product thread have armed, and the parity
+  // of the last phase, for the drain
   uint32_t armed = 0, last_par = 0, next_par = 0;
   auto arm = [&](int i) {
     const uint32_t m = 1u << i;
@@ -269,17 +324,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     last_par = (last_par & ~m) | (next_par & m);
     next_par ^= m;
   };
-  bool ok = true;
-  auto fault = [&](unsigned bit) {
-    atomicOr(&g_fault_prefill, bit);
-    ok = false;
-  };
-  // parity of the next wait on each barrier, kept by every thread
-  uint32_t phase = 0;
-  auto wait = [&](int i, unsigned bit) {  // the same sequence of waits in every thread that waits
-    if (!tc::wait(bar(i), (phase >> i) & 1u, kWaitLimit)) fault(bit);
-  };
-  auto flip = [&](int i) { phase ^= 1u << i; };
 
   float hs[HN];
   const int per = p.nheads / p.ngroups, ppg = (per + 1) / 2;  // heads and pairs per group
@@ -291,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!middle && A.chunk > 0) {
     if (++upair == npairs) { upair = 0; ++useq; }
   }
-  uint32_t it = 0;  // chunks so far: which B buffer is next
+  uint32_t it = 0, itf = 0;  // chunks, and chunks in full, so far
 
   while (stage < 6) {
     // ---- the next run: a unit, its chunks [c0, c1), where its state comes from and goes to
@@ -300,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (stage == 0) {         // middle: the range's own state, from zero
       seq = A.seq; pair = A.pair; c0 = A.chunk; c1 = E.chunk;
       full = from_slot = false;
+      publish = true;
       stage = 1;
     } else if (stage == 1) {  // middle: in full
       seq = A.seq; pair = A.pair; c0 = A.chunk; c1 = E.chunk;
@@ -312,14 +357,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       stage = same ? 6 : 3;
     } else if (stage == 3) {  // whole units
       if (useq == E.seq && upair == E.pair) {
-        stage = 4;
+        stage = A.chunk > 0 ? 4 : 6;
         continue;
       }
       seq = useq; pair = upair; c0 = 0;
       to_slot = true;
       if (++upair == npairs) { upair = 0; ++useq; }
     } else {                  // the last part of the unit at the range's start
-      if (stage == 4 && A.chunk == 0) break;
       seq = A.seq; pair = A.pair; c0 = A.chunk;
       from_slot = false;
       from_carry = true;
@@ -328,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int begin = seq_begin(p.seq, seq), end = seq_end(p.seq, seq, begin);
     if (c1 < 0) c1 = max(1, (end - begin + kQ - 1) / kQ);
+    if (end == begin) c1 = c0;  // nothing to compute, but the state passes through
     int slot = -1;
     if (p.state) {
       slot = claim_slot(p.slots, seq, &g_fault_prefill);
@@ -338,401 +383,474 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int g = pair / ppg, h0 = g * per + 2 * (pair - g * ppg);
     const int nh2 = min(2, g * per + per - h0);  // an odd group's last pair holds one head
-    const int h = h0 + min(wg, nh2 - 1);         // this thread's head for y
-    const bool mine = wg < nh2, owns = hrow < nh2;
-    const float A2 = p.A[h] * kLog2e, Dh = p.D ? p.D[h] : 0.f, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-    const T* dtg = static_cast<const T*>(p.dt) + h;
 
-    auto load = [&](int i, uint32_t off, const CUtensorMap* map, int col, int t, int nblocks) {
-      tc::expect_tx(bar(i), 16384u * nblocks);
-      for (int b = 0; b < nblocks; ++b) tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, t, bar(i));
-      arm(i);
-    };
-    auto load_b = [&](int c, uint32_t k) { load(kBarB0 + (k & 1), L::kB + (k & 1) * L::kTile, &map_b, g * N, begin + c * kQ, N / 64); };
-    auto load_c = [&](int c) { load(kBarC, L::kC, &map_c, g * N, begin + c * kQ, N / 64); };
-    auto load_x = [&](int c) { load(kBarX, L::kX, &map_x, h0 * kP, begin + c * kQ, nh2); };
-    const bool any = end > begin;
-    if (tid == kTma && any) {
-      load_b(c0, it);
-      if (full) load_c(c0);
-      load_x(c0);
-    }
-    T dtn = Elt<T>::from_f(0.f);
-    if (begin + c0 * kQ + row < end) dtn = dtg[(int64_t)(begin + c0 * kQ + row) * p.lddt];
-
-    // ---- the state entering the run
-    float* st = p.state && owns ? p.state + (((size_t)slot * p.nheads + h0) * kP + row) * N + wg * HN : nullptr;
-    if (from_carry) {
-      if (tid == 0 && !middle) {  // the middle's first pass has waited already
-        uint32_t polls = 0, v = 0;
-        do {
-          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flags + me - 1) : "memory");
-        } while (!v && ++polls < kFlagLimit);
-        if (!v) fault(2u);
+    if (warp == kTmaWarp) {
+      // ------------------------------------------------------------ copies
+      if (lane == 0 && c0 < c1) {
+        auto load = [&](int i, uint32_t off, const CUtensorMap* map, int col, int c, int nb) {
+          tc::expect_tx(bar(i), 16384u * nb);
+          for (int b = 0; b < nb; ++b) tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, begin + c * kQ, bar(i));
+          arm(i);
+        };
+        auto load_b = [&](int c, uint32_t k) { load(kBarB + (k & 1), L::kB + (k & 1) * L::kTile, &map_b, g * N, c, N / 64); };
+        auto load_c = [&](int c) { load(kBarC, L::kC, &map_c, g * N, c, N / 64); };
+        auto load_x = [&](int c, uint32_t k) { load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, c, nh2); };
+        auto store_y = [&](int c, uint32_t k) {
+          for (int b = 0; b < nh2; ++b)
+            tc::tma_store_2d(&map_y, (h0 + b) * kP, begin + c * kQ, sb + L::kX + (k & 1) * 32768 + 16384u * b);
+          tc::bulk_commit();
+        };
+        load_b(c0, it);
+        if (full) load_c(c0);
+        load_x(c0, it);
+        for (int c = c0; c < c1 && ok; ++c) {
+          const uint32_t k = it + (c - c0), kf = itf + (c - c0);
+          if (c > c0) {  // the other buffers' last readers, in the chunk before
+            wait(kBarSall, k - 1, 2u);
+            if (full) {
+              wait(kBarY, kf - 1, 2u);
+              if (!ok) break;
+              store_y(c - 1, k - 1);
+            }
+          }
+          if (c + 1 < c1) {
+            load_b(c + 1, k + 1);
+            if (full) tc::bulk_wait_read_all();
+            load_x(c + 1, k + 1);
+            if (full) {
+              wait(kBarYc, kf, 2u);
+              if (!ok) break;
+              load_c(c + 1);
+            }
+          }
+        }
+        const int last = c1 - 1;
+        if (full && ok) {
+          wait(kBarY, itf + (last - c0), 2u);
+          if (ok && begin + (last + 1) * kQ <= end) store_y(last, it + (last - c0));  // a ragged chunk is written below
+        }
+        tc::bulk_wait_read_all();
       }
-      if (__syncthreads_or(!ok)) break;
-      const float4* src = carry + (size_t)(me - 1) * (2 * kP * N / 4);
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------- products
+      if (lane == 0) {
+        for (int c = c0; c < c1 && ok; ++c) {
+          const uint32_t k = it + (c - c0), kf = itf + (c - c0);
+          const uint32_t offB = L::kB + (k & 1) * L::kTile, offX = L::kX + (k & 1) * 32768;
+          wait(kBarB + (k & 1), k >> 1, 1u);
+          if (full) {
+            wait(kBarC, kf, 1u);
+            if (c > c0) wait(kBarY, kf - 1, 2u);  // the accumulators of y are read
+            if (!ok) break;
+            tc::fence_after();
+            const uint64_t dc = tc::desc_sw128(sb + L::kC, 16, 1024), db = tc::desc_sw128(sb + offB, 16, 1024),
+                           dh = tc::desc_sw128(sb + L::kH, 16, 1024);
 #pragma unroll
-      for (int i = 0; i < HN / 4; ++i) {
-        const float4 v = __ldcg(src + i * kThreads + tid);
-        hs[4 * i] = v.x; hs[4 * i + 1] = v.y; hs[4 * i + 2] = v.z; hs[4 * i + 3] = v.w;
-      }
-    } else if (from_slot && st && !(p.slots.fresh && p.slots.fresh[seq])) {
+            for (int kk = 0; kk < N / 16; ++kk) {
+              const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+              tc::mma(tmem + kG, dc + ko, db + ko, kId, kk > 0);
+            }
+            tc::commit(bar(kBarG));
+            arm(kBarG);
+            wait(kBarH, k, 2u);
+            if (!ok) break;
+            tc::fence_after();
 #pragma unroll
-      for (int i = 0; i < HN / 4; ++i) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(st) + i);
-        hs[4 * i] = v.x; hs[4 * i + 1] = v.y; hs[4 * i + 2] = v.z; hs[4 * i + 3] = v.w;
+            for (int kk = 0; kk < N / 16; ++kk) {
+              const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+              tc::mma(tmem + kYc, dc + ko, dh + ko, kId, kk > 0);
+            }
+            tc::commit(bar(kBarYc));
+            arm(kBarYc);
+          } else {
+            wait(kBarH, k, 2u);
+            if (!ok) break;
+          }
+          for (int q = 0; q < 4; ++q) {
+            if (q == 3 && full) {  // the warps finish M before the last quarter of Xw
+              wait(kBarM, kf, 2u);
+              if (!ok) break;
+              tc::fence_after();
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const uint64_t dx = tc::desc_sw128(sb + offX + 16384 * b, 16384, 1024);
+#pragma unroll
+                for (int kk = 0; kk < kQ / 16; ++kk)
+                  tc::mma_ta(tmem + kG + 64 * b, tmem + kM + 64 * b + 8 * kk, dx + kk * (2048 >> 4), kIdYm, kk > 0);
+              }
+              tc::commit(bar(kBarYm));
+              arm(kBarYm);
+            }
+            wait(kBarW, q, 2u);
+            if (!ok) break;
+            tc::fence_after();
+            const uint64_t dbm = tc::desc_sw128(sb + offB + q * 4096, 16384, 1024);
+#pragma unroll
+            for (int s3 = 0; s3 < 3; ++s3) {
+              const uint64_t dw = tc::desc_sw128(sb + L::kW + 8192 * s3, 4096, 1024);
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk)
+                tc::mma(tmem + kS, dw + kk * (2048 >> 4), dbm + kk * (2048 >> 4), kIdS, (q | s3 | kk) != 0);
+            }
+            tc::commit(bar(kBarS));
+            arm(kBarS);
+          }
+          if (!ok) break;
+          tc::commit(bar(kBarSall));
+          arm(kBarSall);
+        }
       }
+      __syncwarp();
     } else {
-#pragma unroll
-      for (int i = 0; i < HN; ++i) hs[i] = 0.f;
-    }
-    // its 16-bit copy, K-major rows of n
-    auto write_copy = [&]() {
-      unsigned char* base = sm + L::kH + (N == 128 ? wg * 16384 : 0);
-      const int cb = N == 128 ? 0 : 4 * wg;
-#pragma unroll
-      for (int c = 0; c < HN / 8; ++c)
-        *reinterpret_cast<uint4*>(base + swz(row, cb + c)) =
-            make_uint4(Pk<T>::pack(hs[8 * c], hs[8 * c + 1]), Pk<T>::pack(hs[8 * c + 2], hs[8 * c + 3]),
-                       Pk<T>::pack(hs[8 * c + 4], hs[8 * c + 5]), Pk<T>::pack(hs[8 * c + 6], hs[8 * c + 7]));
-    };
-    if (full) write_copy();
-    if (nh2 == 1)  // the missing head's x is zero
-      for (int i = tid; i < 1024; i += kThreads) *reinterpret_cast<uint4*>(sm + L::kX + 16384 + 16 * i) = make_uint4(0, 0, 0, 0);
-    tc::fence_proxy_async();
-    tc::fence_before();
-    if (__syncthreads_or(!ok)) break;
-    float psum = 0.f;  // log2 decay of the run so far (head hrow)
-
-    bool stop = false;
-    for (int c = c0; c < c1 && any; ++c, ++it) {
-      const int t0 = begin + c * kQ, nval = min(kQ, end - t0);
-      const bool more = c + 1 < c1;
-      const int bb = kBarB0 + (it & 1);
-      const uint32_t offB = L::kB + (it & 1) * L::kTile;
-      // ---- G and Yc need only B, C and the state copy
-      if (tid == kMma && full) {
-        tc::fence_after();
-        wait(bb, 1u);
-        wait(kBarC, 1u);
-        tc::fence_after();
-        const uint64_t dc = tc::desc_sw128(sb + L::kC, 16, 1024), db = tc::desc_sw128(sb + offB, 16, 1024),
-                       dh = tc::desc_sw128(sb + L::kH, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < N / 16; ++kk) {
-          const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-          tc::mma(tmem + kG, dc + ko, db + ko, kId, kk > 0);
-        }
-        tc::commit(bar(kBarG));
-        arm(kBarG);
-#pragma unroll
-        for (int kk = 0; kk < N / 16; ++kk) {
-          const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-          tc::mma(tmem + kYc, dc + ko, dh + ko, kId, kk > 0);
-        }
-        tc::commit(bar(kBarYc));
-        arm(kBarYc);
-      }
-      __syncwarp();
-      if (tid == kTma && more) load_b(c + 1, it + 1);  // its buffer's last reader, S of the chunk before, is done
-      __syncwarp();
-      // ---- Delta and the decays (thread: head wg, token row)
-      float pre, suf;
-      {
+      // ----------------------------------------------------- compute warps
+      const int h = h0 + min(hd, nh2 - 1);
+      const bool mine = hd < nh2, owns = hrow < nh2;
+      const float A2 = p.A[h] * kLog2e, Dh = p.D ? p.D[h] : 0.f, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+      const T* dtg = static_cast<const T*>(p.dt) + h;
+      T dtn = Elt<T>::from_f(0.f);
+      auto fetch_dt = [&](int c) {
+        const int t = begin + c * kQ + row;
+        if (c < c1 && t < end) dtn = dtg[(int64_t)t * p.lddt];
+      };
+      // Delta and the decays of chunk c (thread: head hd, token row)
+      auto decays = [&](int c, Arrays& a) {
         float d = 0.f;
-        if (row < nval && mine) {
+        if (begin + c * kQ + row < end && mine) {
           const float v = Elt<T>::to_f(dtn) + bias;
           d = p.softplus ? softplus_f(v) : v;
         }
-        const float a = d * A2;
-        pre = a;
-        suf = a;
+        float pre = d * A2, suf = pre;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const float u = __shfl_up_sync(0xffffffffu, pre, o), v = __shfl_down_sync(0xffffffffu, suf, o);
           if (lane >= o) pre += u;
           if (lane + o < 32) suf += v;
         }
-        if (lane == 31) sTot[4 * wg + blk] = pre;
+        if (lane == 31) a.tot[hd][blk] = pre;
         suf = __shfl_down_sync(0xffffffffu, suf, 1);  // the tokens after this one
         if (lane == 31) suf = 0.f;
-        sF[tid] = ex2(suf) * d;
-        sPre[tid] = pre;
-        sDl[tid] = d;
-        if (!kBf16 && tid < 2) sMax[tid] = 0u;
-      }
-      if (more && t0 + kQ + row < end) dtn = dtg[(int64_t)(t0 + kQ + row) * p.lddt];
-      wait(kBarX, 1u);
-      if (nval < kQ) {  // rows behind the sequence belong to others: no NaN of theirs may meet a zero weight
-        wait(bb, 1u);
-        if (full) wait(kBarG, 2u);
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        for (int i = tid; i < (kQ - nval) * 8; i += kThreads) {
-          const uint32_t o = (nval + i / 8) * 128 + (i & 7) * 16;
-#pragma unroll
-          for (int b = 0; b < N / 64; ++b) *reinterpret_cast<uint4*>(sm + offB + 16384 * b + o) = zero;
-          *reinterpret_cast<uint4*>(sm + L::kX + o) = zero;
-          *reinterpret_cast<uint4*>(sm + L::kX + 16384 + o) = zero;
-        }
-        tc::fence_proxy_async();
-      }
-      if (__syncthreads_or(!ok)) { stop = true; break; }
-      float unscale = 1.f;
-      // ---- Xw of 64 tokens as three 16-bit pieces (thread: token tid % 64, 32 columns)
-      const int xr = tid & 63, xh = tid >> 7, xc = ((tid >> 6) & 1) * 4;
-      float scale = 1.f;
-      if constexpr (!kBf16) {  // fp16: the power of two that puts max |x| max Delta below 2^15
-        unsigned m = 0;
-        const int xhead = tid >> 7;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint4 v = *reinterpret_cast<const uint4*>(sm + L::kX + xhead * 16384 + swz(row, k));
-          m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-        }
-        m = max(m & 0xffffu, m >> 16);
-        float wmax = __half2float(__ushort_as_half((unsigned short)m)) * fabsf(sDl[tid]);
-        wmax = wmax < 3.0e38f ? wmax : 1.f;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) wmax = fmaxf(wmax, __shfl_xor_sync(0xffffffffu, wmax, o));
-        if (lane == 0) atomicMax(sMax + xhead, __float_as_uint(wmax));
-        if (__syncthreads_or(!ok)) { stop = true; break; }
-        auto power = [](unsigned m) {  // 2^(14 - exponent of m), within fp32's range
-          const int e = (int)(m >> 23) - 127;
-          return m == 0 ? 0 : min(100, max(-100, 14 - e));
-        };
-        scale = __uint_as_float((unsigned)(127 + power(sMax[xhead])) << 23);
-        unscale = __uint_as_float((unsigned)(127 - power(sMax[hrow])) << 23);
-      }
-      auto write_xw = [&](int half) {
-        const int r = 64 * half + xr;
-        float later = 0.f;
-#pragma unroll
-        for (int b = 1; b < 4; ++b)
-          if (b > (r >> 5)) later += sTot[4 * xh + b];
-        const float w = sF[128 * xh + r] * ex2(later) * scale;
-        const unsigned char* xs = sm + L::kX + xh * 16384;
-        unsigned char* wd = sm + L::kW + xh * 8192;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(xs + swz(r, xc + k));
-          const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
-          uint32_t a[4], b[4], d[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = Pk<T>::unpack(in[e]);
-            const float v0 = f.x * w, v1 = f.y * w;
-            a[e] = Pk<T>::pack(v0, v1);
-            const float2 fa = Pk<T>::unpack(a[e]);
-            const float r0 = v0 - fa.x, r1 = v1 - fa.y;
-            b[e] = Pk<T>::pack(r0, r1);
-            const float2 fb = Pk<T>::unpack(b[e]);
-            d[e] = Pk<T>::pack(r0 - fb.x, r1 - fb.y);
+        a.f[hd][row] = ex2(suf) * d;
+        a.pre[hd][row] = pre;
+        a.dl[hd][row] = d;
+      };
+      auto wait_flag = [&]() {  // the state that the block before publishes
+        if (tid == 0) {
+          uint32_t polls = 0, v = 0;
+          do {
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flags + me - 1) : "memory");
+          } while (!v && ++polls < kFlagLimit);
+          if (!v) {
+            atomicOr(&g_fault_prefill, 2u);
+            s_abort = 1;
+            ok = false;
           }
-          const uint32_t o = swz(xr, xc + k);
-          *reinterpret_cast<uint4*>(wd + o) = make_uint4(a[0], a[1], a[2], a[3]);
-          *reinterpret_cast<uint4*>(wd + 16384 + o) = make_uint4(b[0], b[1], b[2], b[3]);
-          *reinterpret_cast<uint4*>(wd + 32768 + o) = make_uint4(d[0], d[1], d[2], d[3]);
         }
-        tc::fence_proxy_async();
+        return !compute_sync_or(!ok);
       };
-      auto issue_s = [&](int half, int b) {
-        const uint64_t dbm = tc::desc_sw128(sb + offB + half * 8192, 16384, 1024);
+      const float4* const src = carry + (size_t)(me - 1) * (2 * kP * N / 4);
+
+      fetch_dt(c0);
+      // ---- the state entering the run
+      float* st = p.state && owns ? p.state + (((size_t)slot * p.nheads + h0) * kP + row) * N + hd * HN : nullptr;
 #pragma unroll
-        for (int q = 0; q < 3; ++q) {
-          const uint64_t dw = tc::desc_sw128(sb + L::kW + 16384 * q, 8192, 1024);
+      for (int i = 0; i < HN; ++i) hs[i] = 0.f;
+      if (from_carry) {
+        if (!middle) wait_flag();  // the middle's first pass has waited already
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc::mma(tmem + kS, dw + kk * (2048 >> 4), dbm + kk * (2048 >> 4), kIdS, (half | q | kk) != 0);
+        for (int i = 0; i < HN / 4; ++i) {
+          const float4 v = __ldcg(src + i * kCompute + tid);
+          hs[4 * i] = v.x; hs[4 * i + 1] = v.y; hs[4 * i + 2] = v.z; hs[4 * i + 3] = v.w;
         }
-        tc::commit(bar(b));
-        arm(b);
-      };
-      write_xw(0);
-      if (__syncthreads_or(!ok)) { stop = true; break; }
-      if (tid == kMma) {
-        if (!full) wait(bb, 1u);
-        tc::fence_after();
-        issue_s(0, kBarS0);
+      } else if (from_slot && st && !(p.slots.fresh && p.slots.fresh[seq])) {
+#pragma unroll
+        for (int i = 0; i < HN / 4; ++i) {
+          const float4 v = __ldcs(reinterpret_cast<const float4*>(st) + i);
+          hs[4 * i] = v.x; hs[4 * i + 1] = v.y; hs[4 * i + 2] = v.z; hs[4 * i + 3] = v.w;
+        }
       }
-      __syncwarp();
-      // ---- M_h, row `row`, head wg
-      if (full) {
-        wait(kBarG, 2u);
-        tc::fence_after();
-        float between = 0.f;  // log2 decay of the blocks between j's and i's
-        for (int j = blk; j >= 0; --j) {
+      // its 16-bit copy: K-major, row = state row
+      auto write_copy = [&]() {
+        const int n0 = hd * HN;
+        unsigned char* base = sm + L::kH + (n0 / 64) * 16384;
+#pragma unroll
+        for (int k = 0; k < HN / 8; ++k)
+          *reinterpret_cast<uint4*>(base + swz(row, (n0 % 64) / 8 + k)) = pack8<T>(hs + 8 * k);
+      };
+      auto signal = [&](int i) {  // generic and TMEM accesses of the warp, then one arrival
+        tc::fence_proxy_async();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(bar(i));
+      };
+      if (c0 < c1) {
+        if (full) write_copy();
+        if (nh2 == 1)  // the missing head's x is zero
+          for (int i = tid; i < 2048; i += kCompute)
+            *reinterpret_cast<uint4*>(sm + L::kX + (i >> 10) * 32768 + 16384 + 16 * (i & 1023)) = make_uint4(0, 0, 0, 0);
+        decays(c0, arr[it & 1]);
+        fetch_dt(c0 + 1);
+        signal(kBarH);
+        compute_sync_or(false);
+      }
+      float psum = 0.f;  // log2 decay of the run so far (head hrow)
+
+      for (int c = c0; c < c1; ++c) {
+        const uint32_t k = it + (c - c0), kf = itf + (c - c0);
+        const int t0 = begin + c * kQ, nval = min(kQ, end - t0);
+        const bool more = c + 1 < c1;
+        const Arrays& a = arr[k & 1];
+        unsigned char* const xs = sm + L::kX + (k & 1) * 32768;
+        wait(kBarX + (k & 1), k >> 1, 1u);
+        if (nval < kQ) {  // rows behind the sequence belong to others: no NaN of theirs may meet a zero weight
+          wait(kBarB + (k & 1), k >> 1, 1u);
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          for (int i = tid; i < (kQ - nval) * 8; i += kCompute) {
+            const uint32_t o = (nval + i / 8) * 128 + (i & 7) * 16;
+#pragma unroll
+            for (int b = 0; b < N / 64; ++b) *reinterpret_cast<uint4*>(sm + L::kB + (k & 1) * L::kTile + 16384 * b + o) = zero;
+            *reinterpret_cast<uint4*>(xs + o) = zero;
+            *reinterpret_cast<uint4*>(xs + 16384 + o) = zero;
+          }
+          compute_sync_or(false);
+        }
+        float scale = 1.f, unscale = 1.f;
+        const int xc = 2 * blk;  // Xw: 16 columns of head hd, lanes over tokens
+        if constexpr (!kBf16) {  // fp16: the power of two that puts max (|x| Delta) below 2^15
+          if (tid < 2) sMax[tid] = 0u;
+          compute_sync_or(false);
+          unsigned m = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint4 v = *reinterpret_cast<const uint4*>(xs + hd * 16384 + swz(row, j));
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+          }
+          m = max(m & 0xffffu, m >> 16);
+          float top = __half2float(__ushort_as_half((unsigned short)m)) * fabsf(a.dl[hd][row]);
+          top = top < 3.0e38f ? top : 1.f;
+#pragma unroll
+          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (lane == 0) atomicMax(sMax + hd, __float_as_uint(top));
+          compute_sync_or(false);
+          auto power = [](unsigned v) {  // 2^(14 - exponent of v), within fp32's range
+            const int e = (int)(v >> 23) - 127;
+            return v == 0 ? 0 : min(100, max(-100, 14 - e));
+          };
+          scale = __uint_as_float((unsigned)(127 + power(sMax[hd])) << 23);
+          unscale = __uint_as_float((unsigned)(127 - power(sMax[hrow])) << 23);
+        }
+        // ---- 32 tokens of Xw as three 16-bit pieces
+        auto write_xw = [&](int q) {
+          float later = 0.f;
+          for (int b = q + 1; b < 4; ++b) later += a.tot[hd][b];
+          const float w = a.f[hd][32 * q + lane] * ex2(later) * scale;
+          const f2_t w2 = pk2(w, w), minus = pk2(-1.f, -1.f);
+          uint32_t u[8], v[8], z[8];
+#pragma unroll
+          for (int k2 = 0; k2 < 2; ++k2) {
+            const uint4 xv = *reinterpret_cast<const uint4*>(xs + hd * 16384 + swz(32 * q + lane, xc + k2));
+            const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = Pk<T>::unpack(in[e]);
+              const f2_t x0 = mul2(pk2(f.x, f.y), w2);
+              const uint32_t p0 = Pk<T>::pack(lo2(x0), hi2(x0));
+              const float2 f0 = Pk<T>::unpack(p0);
+              const f2_t x1 = fma2(pk2(f0.x, f0.y), minus, x0);
+              const uint32_t p1 = Pk<T>::pack(lo2(x1), hi2(x1));
+              const float2 f1 = Pk<T>::unpack(p1);
+              const f2_t x2 = fma2(pk2(f1.x, f1.y), minus, x1);
+              u[4 * k2 + e] = p0;
+              v[4 * k2 + e] = p1;
+              z[4 * k2 + e] = Pk<T>::pack(lo2(x2), hi2(x2));
+            }
+          }
+          if (q > 0) wait(kBarS, q - 1, 2u);  // the products of the quarter before have read the buffer
+#pragma unroll
+          for (int k2 = 0; k2 < 2; ++k2) {
+            unsigned char* wd = sm + L::kW + hd * 4096 + swz(lane, xc + k2);
+            *reinterpret_cast<uint4*>(wd) = make_uint4(u[4 * k2], u[4 * k2 + 1], u[4 * k2 + 2], u[4 * k2 + 3]);
+            *reinterpret_cast<uint4*>(wd + 8192) = make_uint4(v[4 * k2], v[4 * k2 + 1], v[4 * k2 + 2], v[4 * k2 + 3]);
+            *reinterpret_cast<uint4*>(wd + 16384) = make_uint4(z[4 * k2], z[4 * k2 + 1], z[4 * k2 + 2], z[4 * k2 + 3]);
+          }
+          signal(kBarW);
+        };
+        // ---- columns 32 j .. of M, row `row`, head hd
+        const float pre = a.pre[hd][row];
+        auto write_m = [&](int j) {
           float gv[32];
           tc::ld32x32b_x32(tmem + lane_base + kG + 32 * j, gv);
           uint32_t mp[16];
           if (j == blk) {
-            const float4* pr = reinterpret_cast<const float4*>(sPre + 128 * wg + 32 * j);
-            const float4* dl = reinterpret_cast<const float4*>(sDl + 128 * wg + 32 * j);
+            const float4* pr = reinterpret_cast<const float4*>(a.pre[hd] + 32 * j);
+            const float4* dl = reinterpret_cast<const float4*>(a.dl[hd] + 32 * j);
+            const f2_t pre2 = pk2(pre, pre), minus = pk2(-1.f, -1.f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 pv = pr[k], dv = dl[k];
-              float m[4] = {gv[4 * k] * ex2(pre - pv.x) * dv.x, gv[4 * k + 1] * ex2(pre - pv.y) * dv.y,
-                            gv[4 * k + 2] * ex2(pre - pv.z) * dv.z, gv[4 * k + 3] * ex2(pre - pv.w) * dv.w};
+            for (int i = 0; i < 8; ++i) {
+              const float4 pv = pr[i], dv = dl[i];
+              const f2_t m01 = mul2(mul2(pk2(gv[4 * i], gv[4 * i + 1]), ex2_2(fma2(pk2(pv.x, pv.y), minus, pre2))), pk2(dv.x, dv.y));
+              const f2_t m23 = mul2(mul2(pk2(gv[4 * i + 2], gv[4 * i + 3]), ex2_2(fma2(pk2(pv.z, pv.w), minus, pre2))), pk2(dv.z, dv.w));
+              float m[4] = {lo2(m01), hi2(m01), lo2(m23), hi2(m23)};
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (4 * k + e > lane) m[e] = 0.f;
-              mp[2 * k] = Pk<T>::pack(m[0], m[1]);
-              mp[2 * k + 1] = Pk<T>::pack(m[2], m[3]);
+                if (4 * i + e > lane) m[e] = 0.f;
+              mp[2 * i] = Pk<T>::pack(m[0], m[1]);
+              mp[2 * i + 1] = Pk<T>::pack(m[2], m[3]);
             }
           } else {
-            const float ei = ex2(pre + between);
-            between += sTot[4 * wg + j];
-            const float4* fj = reinterpret_cast<const float4*>(sF + 128 * wg + 32 * j);
+            float x = pre;  // from the end of block j to this row
+            for (int b = j + 1; b < blk; ++b) x += a.tot[hd][b];
+            const float ei = ex2(x);
+            const f2_t ei2 = pk2(ei, ei);
+            const float4* fj = reinterpret_cast<const float4*>(a.f[hd] + 32 * j);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 fv = fj[k];
-              mp[2 * k] = Pk<T>::pack(gv[4 * k] * (ei * fv.x), gv[4 * k + 1] * (ei * fv.y));
-              mp[2 * k + 1] = Pk<T>::pack(gv[4 * k + 2] * (ei * fv.z), gv[4 * k + 3] * (ei * fv.w));
+            for (int i = 0; i < 8; ++i) {
+              const float4 fv = fj[i];
+              const f2_t m01 = mul2(pk2(gv[4 * i], gv[4 * i + 1]), mul2(ei2, pk2(fv.x, fv.y)));
+              const f2_t m23 = mul2(pk2(gv[4 * i + 2], gv[4 * i + 3]), mul2(ei2, pk2(fv.z, fv.w)));
+              mp[2 * i] = Pk<T>::pack(lo2(m01), hi2(m01));
+              mp[2 * i + 1] = Pk<T>::pack(lo2(m23), hi2(m23));
             }
           }
-          tc::st32x32b_x16(tmem + lane_base + kM + 64 * wg + 16 * j, mp);
-        }
-        tc::st_wait();
-      }
-      wait(kBarS0, 2u);
-      write_xw(1);
-      tc::fence_before();
-      if (__syncthreads_or(!ok)) { stop = true; break; }
-      if (tid == kMma) {
-        tc::fence_after();
+          tc::st32x32b_x16(tmem + lane_base + kM + 64 * hd + 16 * j, mp);
+        };
+        write_xw(0);
         if (full) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint64_t dx = tc::desc_sw128(sb + L::kX + 16384 * q, 16384, 1024);
-#pragma unroll
-            for (int kk = 0; kk < kQ / 16; ++kk)
-              tc::mma_ta(tmem + kG + 64 * q, tmem + kM + 64 * q + 8 * kk, dx + kk * (2048 >> 4), kIdYm, kk > 0);
-          }
-          tc::commit(bar(kBarYm));
-          arm(kBarYm);
+          wait(kBarG, kf, 2u);
+          tc::fence_after();
+          write_m(blk);
         }
-        issue_s(1, kBarS1);
-      }
-      __syncwarp();
-      // ---- y = (2^cs Yc + Ym + D x) SiLU(z)
-      if (full) {
-        wait(kBarYc, 2u);
-        if (tid == kTma && more) load_c(c + 1);
-        wait(kBarYm, 2u);
-        if (tid == kTma && more) load_x(c + 1);
-        __syncwarp();
-        tc::fence_after();
-        float cs = pre;
-        for (int b = 0; b < blk; ++b) cs += sTot[4 * wg + b];
-        const float e = ex2(cs);
-        const bool out = row < nval && mine;
-        const int64_t t = t0 + row;
-        const T* xg = static_cast<const T*>(p.x) + t * p.ldx + h * kP;
-        const T* zg = p.z ? static_cast<const T*>(p.z) + t * p.ldz + h * kP : nullptr;
-        T* yg = static_cast<T*>(p.y) + (t * p.nheads + h) * kP;
+        write_xw(1);
+        if (full && blk >= 1) write_m(blk - 1);
+        write_xw(2);
+        if (full) {
+          if (blk >= 2) write_m(blk - 2);
+          if (blk >= 3) write_m(blk - 3);
+          tc::st_wait();
+          signal(kBarM);
+        }
+        write_xw(3);
+        if (more) decays(c + 1, arr[(k + 1) & 1]);
+        fetch_dt(c + 2);
+        // ---- y = (2^cs Yc + Ym + D x) SiLU(z), in place of x
+        if (full) {
+          float cs = pre;
+          for (int b = 0; b < blk; ++b) cs += a.tot[hd][b];
+          const float e = ex2(cs);
+          const f2_t e2 = pk2(e, e), D2 = pk2(Dh, Dh);
+          const int64_t t = t0 + row;
+          const T* zg = p.z && mine && row < nval ? static_cast<const T*>(p.z) + t * p.ldz + h * kP : nullptr;
+          wait(kBarYc, kf, 2u);
+          wait(kBarYm, kf, 2u);
+          wait(kBarW, 3, 2u);  // every warp has read its x
+          tc::fence_after();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float yc[16], ym[16];
-          tc::ld32x32b_x16(tmem + lane_base + kYc + 64 * wg + 16 * k, yc);
-          tc::ld32x32b_x16(tmem + lane_base + kG + 64 * wg + 16 * k, ym);
-          if (out) {
+          for (int i = 0; i < 4; ++i) {
+            float yc[16], ym[16];
+            tc::ld32x32b_x16(tmem + lane_base + kYc + 64 * hd + 16 * i, yc);
+            tc::ld32x32b_x16(tmem + lane_base + kG + 64 * hd + 16 * i, ym);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              float xv[8], o[8];
-              load8(xg + 16 * k + 8 * u, xv);
+              uint4* at = reinterpret_cast<uint4*>(xs + hd * 16384 + swz(row, 2 * i + u));
+              const uint4 xv = *at;
+              const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
+              float o[8];
 #pragma unroll
-              for (int v = 0; v < 8; ++v) o[v] = fmaf(Dh, xv[v], fmaf(e, yc[8 * u + v], ym[8 * u + v]));
-              if (zg) {
-#pragma unroll
-                for (int v = 0; v < 8; ++v) {
-                  const float zv = ldf(zg + 16 * k + 8 * u + v);
-                  o[v] *= zv * sigmoid_f(zv);
-                }
+              for (int v = 0; v < 4; ++v) {
+                const float2 f = Pk<T>::unpack(in[v]);
+                const int at8 = 8 * u + 2 * v;
+                const f2_t r = fma2(D2, pk2(f.x, f.y), fma2(e2, pk2(yc[at8], yc[at8 + 1]), pk2(ym[at8], ym[at8 + 1])));
+                o[2 * v] = lo2(r);
+                o[2 * v + 1] = hi2(r);
               }
-              store8(yg + 16 * k + 8 * u, o);
+              if (zg) {
+                float zv[8];
+                if (p.zvec) load8(zg + 16 * i + 8 * u, zv);
+                else
+#pragma unroll
+                  for (int v = 0; v < 8; ++v) zv[v] = ldf(zg + 16 * i + 8 * u + v);
+#pragma unroll
+                for (int v = 0; v < 8; ++v) o[v] *= zv[v] * sigmoid_f(zv[v]);
+              }
+              if (mine) *at = pack8<T>(o);
+            }
+          }
+          signal(kBarY);
+          if (nval < kQ) {  // the rows of a ragged chunk, one by one
+            compute_sync_or(false);
+            for (int i = tid; i < nval * 8 * nh2; i += kCompute) {
+              const int hh = i / (nval * 8), r = (i >> 3) - hh * nval, cc = i & 7;
+              const uint4 v = *reinterpret_cast<const uint4*>(xs + hh * 16384 + swz(r, cc));
+              *reinterpret_cast<uint4*>(static_cast<T*>(p.y) + ((int64_t)(t0 + r) * p.nheads + h0 + hh) * kP + 8 * cc) = v;
             }
           }
         }
-      }
-      // ---- H <- 2^cs_last H + S
-      wait(kBarS1, 2u);
-      if (!full && tid == kTma && more) load_x(c + 1);
-      __syncwarp();
-      tc::fence_after();
-      {
-        const float tot = (sTot[4 * hrow] + sTot[4 * hrow + 1]) + (sTot[4 * hrow + 2] + sTot[4 * hrow + 3]);
-        psum += tot;
-        const float dec = ex2(tot);
+        // ---- H <- 2^cs_last H + S
+        wait(kBarSall, k, 2u);
+        tc::fence_after();
+        {
+          const float tot = (a.tot[hrow][0] + a.tot[hrow][1]) + (a.tot[hrow][2] + a.tot[hrow][3]);
+          psum += tot;
+          const float dec = ex2(tot);
 #pragma unroll
-        for (int k = 0; k < HN; k += 16) {
-          float sv[16];
-          tc::ld32x32b_x16(tmem + lane_base + kS + wg * HN + k, sv);
+          for (int n = 0; n < HN; n += 16) {
+            float sv[16];
+            tc::ld32x32b_x16(tmem + lane_base + kS + hd * HN + n, sv);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) hs[k + i] = fmaf(dec, hs[k + i], kBf16 ? sv[i] : sv[i] * unscale);
+            for (int i = 0; i < 16; ++i) hs[n + i] = fmaf(dec, hs[n + i], kBf16 ? sv[i] : sv[i] * unscale);
+          }
         }
-        if (full && more) write_copy();  // C H^T of this chunk is done with the old copy
+        if (more) {
+          if (full) write_copy();  // C H^T of this chunk is done with the old copy
+          signal(kBarH);
+        }
+        if (compute_sync_or(!ok)) {
+          ok = false;
+          break;
+        }
       }
-      flip(bb);
-      flip(kBarX);
-      flip(kBarS0);
-      flip(kBarS1);
-      if (full) {
-        flip(kBarC);
-        flip(kBarG);
-        flip(kBarYc);
-        flip(kBarYm);
-      }
-      tc::fence_proxy_async();
-      tc::fence_before();
-      if (__syncthreads_or(!ok)) { stop = true; break; }
-      tc::fence_after();
-    }
-    if (stop) break;
 
-    // ---- the state leaving the run
-    if (!full) {  // the middle of a unit: add what enters it, decayed
-      if (tid == 0) {
-        uint32_t polls = 0, v = 0;
-        do {
-          asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flags + me - 1) : "memory");
-        } while (!v && ++polls < kFlagLimit);
-        if (!v) fault(2u);
+      // ---- the state leaving the run
+      if (!full && ok) {  // the middle of a unit: add what enters it, decayed
+        if (wait_flag()) {
+          const float dec = ex2(psum);
+#pragma unroll
+          for (int i = 0; i < HN / 4; ++i) {
+            const float4 v = __ldcg(src + i * kCompute + tid);
+            hs[4 * i] = fmaf(dec, v.x, hs[4 * i]);
+            hs[4 * i + 1] = fmaf(dec, v.y, hs[4 * i + 1]);
+            hs[4 * i + 2] = fmaf(dec, v.z, hs[4 * i + 2]);
+            hs[4 * i + 3] = fmaf(dec, v.w, hs[4 * i + 3]);
+          }
+        }
       }
-      if (__syncthreads_or(!ok)) break;
-      const float dec = ex2(psum);
-      const float4* src = carry + (size_t)(me - 1) * (2 * kP * N / 4);
+      if (publish) {
+        float4* dst = carry + (size_t)me * (2 * kP * N / 4);
 #pragma unroll
-      for (int i = 0; i < HN / 4; ++i) {
-        const float4 v = __ldcg(src + i * kThreads + tid);
-        hs[4 * i] = fmaf(dec, v.x, hs[4 * i]);
-        hs[4 * i + 1] = fmaf(dec, v.y, hs[4 * i + 1]);
-        hs[4 * i + 2] = fmaf(dec, v.z, hs[4 * i + 2]);
-        hs[4 * i + 3] = fmaf(dec, v.w, hs[4 * i + 3]);
+        for (int i = 0; i < HN / 4; ++i)
+          dst[i * kCompute + tid] = make_float4(hs[4 * i], hs[4 * i + 1], hs[4 * i + 2], hs[4 * i + 3]);
+        __threadfence();
+        compute_sync_or(false);
+        if (tid == 0) asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(flags + me) : "memory");
+      } else if (to_slot && st) {
+#pragma unroll
+        for (int i = 0; i < HN / 4; ++i)
+          __stcs(reinterpret_cast<float4*>(st) + i, make_float4(hs[4 * i], hs[4 * i + 1], hs[4 * i + 2], hs[4 * i + 3]));
       }
-      publish = true;
     }
-    if (publish) {
-      float4* dst = carry + (size_t)me * (2 * kP * N / 4);
-#pragma unroll
-      for (int i = 0; i < HN / 4; ++i)
-        dst[i * kThreads + tid] = make_float4(hs[4 * i], hs[4 * i + 1], hs[4 * i + 2], hs[4 * i + 3]);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(flags + me) : "memory");
-    } else if (to_slot && st) {
-#pragma unroll
-      for (int i = 0; i < HN / 4; ++i)
-        __stcs(reinterpret_cast<float4*>(st) + i, make_float4(hs[4 * i], hs[4 * i + 1], hs[4 * i + 2], hs[4 * i + 3]));
-    }
+    it += c1 - c0;
+    if (full) itf += c1 - c0;
+    if (__syncthreads_or(!ok)) break;
   }
 
   // Drain: copies and products in flight must be done before shared memory and
-  // TMEM are given back (a no-op on the normal path).
-  if (tid == kMma || tid == kTma) {
+  // TMEM are given back (a no-op on the normal path, but for the last y).
+  if (lane == 0 && warp >= 8) {
 #pragma unroll
-    for (int i = 0; i < kNumBars; ++i)
+    for (int i = 0; i < kBarW; ++i)
       if ((armed >> i) & 1u)
         if (!tc::wait(bar(i), (last_par >> i) & 1u, kWaitLimit)) atomicOr(&g_fault_prefill, 4u);
+    tc::bulk_wait_all();
   }
   tc::fence_before();
   __syncthreads();
@@ -746,7 +864,8 @@ int pairs(const SsdPrefillParams& p) { return p.ngroups * ((p.nheads / p.ngroups
 
 template <typename T, int N>
 cudaError_t run(const SsdPrefillParams& p, cudaStream_t s) {
-  CUtensorMap mx, mb, mc;
+  CUtensorMap mx, mb, mc, my;
+  std::memset(&my, 0, sizeof(my));
   std::memset(&mx, 0, sizeof(mx));
   std::memset(&mb, 0, sizeof(mb));
   std::memset(&mc, 0, sizeof(mc));
@@ -754,7 +873,8 @@ cudaError_t run(const SsdPrefillParams& p, cudaStream_t s) {
   if (p.seq.tokens > 0 &&  // without tokens the maps are never used
       (!tc::encode_2d(&mx, bf, p.x, (int64_t)p.nheads * kP, p.seq.tokens, p.ldx, kQ) ||
        !tc::encode_2d(&mb, bf, p.B, (int64_t)p.ngroups * N, p.seq.tokens, p.ldb, kQ) ||
-       !tc::encode_2d(&mc, bf, p.C, (int64_t)p.ngroups * N, p.seq.tokens, p.ldc, kQ)))
+       !tc::encode_2d(&mc, bf, p.C, (int64_t)p.ngroups * N, p.seq.tokens, p.ldc, kQ) ||
+       !tc::encode_2d(&my, bf, p.y, (int64_t)p.nheads * kP, p.seq.tokens, (int64_t)p.nheads * kP, kQ)))
     return cudaErrorInvalidValue;
   const int npairs = pairs(p), blocks = prefill_blocks(p.seq.tokens, p.seq.nseq, npairs, p.sms);
   prefill_plan_kernel<<<1, 1024, 0, s>>>(p, npairs, blocks);
@@ -773,7 +893,7 @@ cudaError_t run(const SsdPrefillParams& p, cudaStream_t s) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<T, N>, p, npairs, blocks, mx, mb, mc);
+  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<T, N>, p, npairs, blocks, mx, mb, mc, my);
 }
 
 template <typename T>
