@@ -51,6 +51,7 @@ __device__ __forceinline__ RaggedTile ragged_tile(const Ragged& r, long long v, 
 __device__ __forceinline__ void check_offsets(const Ragged& r, unsigned* fault) {
   if (!r.cu) return;
   bool bad = false;
+#pragma unroll 1
   for (int i = threadIdx.x; i <= r.nseq; i += blockDim.x) {
     const int c = r.cu[i];
     bad |= c < 0 || c > r.tokens || (i > 0 && c < r.cu[i - 1]);
@@ -68,6 +69,7 @@ __device__ __forceinline__ int claim_slot(const Slots& s, int i, unsigned* fault
   const int slot = s.index[i];
   bool bad = slot >= s.count;
   if (slot >= 0 && !bad)
+#pragma unroll 1
     for (int j = threadIdx.x; j < i; j += blockDim.x) bad |= s.index[j] == slot;
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) atomicOr(fault, 8u);

@@ -67,9 +67,13 @@ namespace {
 
 constexpr int kP = 64;         // head dimension
 constexpr int kQ = 128;        // chunk length
-constexpr int kCompute = 256;  // threads of the 8 compute warps
-constexpr int kMmaWarp = 8, kTmaWarp = 9;
-constexpr int kThreads = kCompute + 64;
+// Warps: 0-7 form M and y (a warpgroup per head), 8-11 Xw and the state, then
+// one for the products, one for the copies and one per head for the decays.  The registers of a block, 128 per thread at launch, are split
+// unevenly: the state's warps hold a whole state row each.
+constexpr int kGroupY = 256, kGroupS = 128;  // threads of the two groups
+constexpr int kMmaWarp = 12, kTmaWarp = 13, kDecayWarp = 14;  // and 15
+constexpr int kThreads = 512;
+constexpr int kRegsS = 200, kRegsHelp = 56;  // 2 x 128 + 200 + 56 = 4 x 128 per quarter of the SM
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr uint32_t kFlagLimit = 1u << 22;  // polls of a predecessor's flag
 constexpr uint32_t kG = 0, kYc = 128, kM = 256, kS = 384;  // TMEM columns (Ym over G)
@@ -166,7 +170,7 @@ struct Lay {
   static constexpr int kArr = kH + kTile;             // two of Arrays
   static constexpr int kMax = kArr + 2 * 3104;        // unsigned [2]: largest |x| Delta of the chunk (fp16)
   static constexpr int kBars = kMax + 16;             // mbarriers
-  static constexpr int kSlot = kBars + 128;
+  static constexpr int kSlot = kBars + 176;  // TMEM base address
   static constexpr int kBytes = kSlot + 16;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -178,21 +182,29 @@ struct Arrays {      // per head of the pair and token of the chunk
 };
 static_assert(sizeof(Arrays) == 3104, "Lay::kMax");
 
-// mbarriers: copies landed; products done; 8 warps' arrivals
+// mbarriers: copies landed; products done; arrivals of the warps of a group.
+// A parity names a phase only to a thread that can be neither a phase behind
+// nor one ahead.  The pairs [2] alternate between chunks (or chunks in full,
+// for those of y), because their waiters and the next chunk's signallers are
+// not ordered more tightly; kBarS and kBarW have four phases per chunk, each of
+// which is waited for; the others have one per chunk in full.
 enum : int {
   kBarB = 0,      // [2]
   kBarX = 2,      // [2]
-  kBarC = 4,
-  kBarG = 5,      // G
-  kBarYc = 6,     // C H^T
-  kBarYm = 7,     // M X
-  kBarS = 8,      // a quarter of S has read its Xw: four phases a chunk
-  kBarSall = 9,   // all of S
-  kBarW = 10,     // a quarter of Xw is written: four phases a chunk
-  kBarM = 11,     // M is written
-  kBarH = 12,     // the state copy is written and the accumulators are read: the next chunk's products may start
-  kBarY = 13,     // y is in place of x
-  kNumBars = 14
+  kBarSall = 4,   // [2] all of S (for the copies)
+  kBarC = 6,
+  kBarG = 7,      // G
+  kBarYc = 8,     // C H^T
+  kBarYm = 9,     // M X
+  kBarS = 10,     // a quarter of S is done, and with its Xw
+  kNumTx = 11,    // those above are armed by the copy and product threads
+  kBarA = 11,     // [2] the decays are written
+  kBarW = 13,     // a quarter of Xw is written
+  kBarM = 14,     // M is written
+  kBarR = 15,     // [2] Xw's warps are done with x
+  kBarH = 17,     // [2] the state copy is written and S is read: the next chunk's products may start
+  kBarY = 19,     // [2] y is in place of x, its accumulators are read
+  kNumBars = 21
 };
 
 __device__ __forceinline__ uint32_t swz(int r, int c) {
@@ -201,15 +213,28 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-// Barrier of the compute warps; true everywhere if any thread's flag is set.
-__device__ __forceinline__ bool compute_sync_or(bool v) {
+// Barriers of the y group and of the state group; the latter is true everywhere if any thread's flag is set.
+__device__ __forceinline__ void sync_y() { asm volatile("barrier.cta.sync 1, 256;\n" ::: "memory"); }
+__device__ __forceinline__ bool sync_s(bool v) {
   int r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 256, p;\n selp.b32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 2, 128, p;\n selp.b32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
       : "r"((int)v)
       : "memory");
   return r != 0;
+}
+// 32 bytes of one thread, 32-byte aligned.
+__device__ __forceinline__ void ld_v8(const float* p, float* v) {
+  asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st_v8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};\n" ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "l"(p)
+               : "memory");
 }
 
 template <typename T> struct Pk;
@@ -246,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kId = tc::idesc_f16(kBf16, 128, 128, false, false);  // G, Yc
   constexpr uint32_t kIdS = tc::idesc_f16(kBf16, 128, N, true, true);
   constexpr uint32_t kIdYm = tc::idesc_f16(kBf16, 128, 64, false, true);
-  constexpr int HN = N / 2;          // state columns per thread
 
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = tc::saddr(smem_raw);
@@ -261,14 +285,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return sb + L::kBars + 8u * static_cast<uint32_t>(i); };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // compute warps: TMEM lane = row; a warpgroup per head of the pair
+  // the groups: TMEM lane = row; a warpgroup of the y group per head of the pair
   const int hd = (warp >> 2) & 1, blk = warp & 3, row = 32 * blk + lane;
   const uint32_t lane_base = static_cast<uint32_t>(32 * blk) << 16;
   const int hrow = row >> 6;         // the head of state row `row`
 
   if (tid == 0) {
 #pragma unroll
-    for (int i = 0; i < kNumBars; ++i) tc::mbar_init(bar(i), i >= kBarW ? 8 : 1);
+    for (int i = 0; i < kNumBars; ++i) tc::mbar_init(bar(i), i < kNumTx ? 1 : i < kBarW ? 2 : i == kBarM || i >= kBarY ? 8 : 4);
     tc::fence_mbar_init();
     s_abort = 0;
   }
@@ -303,18 +327,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A wait that runs out, or that another thread's has, makes `ok` false; the
   // thread goes on to the next place where its role leaves the loop.
   bool ok = true;
-  auto wait = [&](int i, uint32_t parity, unsigned bit) {
-    if (tc::wait(bar(i), parity & 1u, 1)) return;
-    for (uint32_t n = 0; ok && n < kWaitLimit; ++n) {
-      if (tc::wait(bar(i), parity & 1u, 1)) return;
+  auto wait = [&](int i, uint32_t parity, int bit) {
+    uint32_t n = 0;
+    while (ok && !tc::wait(bar(i), parity & 1u, 1)) {
+      if (++n == kWaitLimit) s_abort = bit;
       if (*reinterpret_cast<volatile int*>(&s_abort)) ok = false;
     }
-    if (ok) {
-      atomicOr(&g_fault_prefill, bit);
-      s_abort = 1;
-      ok = false;
-    }
   };
+  // the pairs that alternate between chunks
+  auto wait2 = [&](int i, uint32_t k, int bit) { wait(i + (int)(k & 1), k >> 1, bit); };
   // barriers that the copy and the product thread have armed, and the parity
   // of the last phase, for the drain
   uint32_t armed = 0, last_par = 0, next_par = 0;
@@ -325,7 +346,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     next_par ^= m;
   };
 
-  float hs[HN];
+  auto signal = [&](int i) {  // the warp's shared-memory and TMEM accesses, then one arrival
+    tc::fence_proxy_async();
+    tc::fence_before();
+    __syncwarp();
+    if (lane == 0) arrive(bar(i));
+  };
   const int per = p.nheads / p.ngroups, ppg = (per + 1) / 2;  // heads and pairs per group
   const bool same = A.seq == E.seq && A.pair == E.pair;
   const bool middle = same && A.chunk > 0 && E.chunk > 0;
@@ -337,523 +363,587 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   uint32_t it = 0, itf = 0;  // chunks, and chunks in full, so far
 
-  while (stage < 6) {
-    // ---- the next run: a unit, its chunks [c0, c1), where its state comes from and goes to
-    int seq, pair, c0, c1 = -1;
-    bool full = true, from_slot = true, from_carry = false, publish = false, to_slot = false;
-    if (stage == 0) {         // middle: the range's own state, from zero
-      seq = A.seq; pair = A.pair; c0 = A.chunk; c1 = E.chunk;
-      full = from_slot = false;
-      publish = true;
-      stage = 1;
-    } else if (stage == 1) {  // middle: in full
-      seq = A.seq; pair = A.pair; c0 = A.chunk; c1 = E.chunk;
-      from_slot = false;
-      from_carry = true;
-      stage = 6;
-    } else if (stage == 2) {  // the first part of the unit at the range's end
-      seq = E.seq; pair = E.pair; c0 = 0; c1 = E.chunk;
-      publish = true;
-      stage = same ? 6 : 3;
-    } else if (stage == 3) {  // whole units
-      if (useq == E.seq && upair == E.pair) {
-        stage = A.chunk > 0 ? 4 : 6;
-        continue;
+  // The next run: a unit, its chunks [c0, c0 + n), where its state comes from
+  // and goes to.  All threads of the block call it in step.
+  struct Run {
+    int seq, c0, n, begin, end, slot, g, h0, nh2;
+    bool full, from_slot, from_carry, publish, to_slot;
+    __device__ __forceinline__ int t0(int j) const { return begin + (c0 + j) * kQ; }
+  } run;
+  auto next = [&]() -> bool {
+    while (stage < 6) {
+      int pair, c1 = -1;
+      run.full = run.from_slot = true;
+      run.from_carry = run.publish = run.to_slot = false;
+      if (stage <= 1) {         // middle: the range's own state, from zero; then in full
+        run.seq = A.seq; pair = A.pair; run.c0 = A.chunk; c1 = E.chunk;
+        run.from_slot = false;
+        run.full = run.from_carry = stage == 1;
+        run.publish = stage == 0;
+        stage = stage == 0 ? 1 : 6;
+      } else if (stage == 2) {  // the first part of the unit at the range's end
+        run.seq = E.seq; pair = E.pair; run.c0 = 0; c1 = E.chunk;
+        run.publish = true;
+        stage = same ? 6 : 3;
+      } else if (stage == 3) {  // whole units
+        if (useq == E.seq && upair == E.pair) {
+          stage = A.chunk > 0 ? 4 : 6;
+          continue;
+        }
+        run.seq = useq; pair = upair; run.c0 = 0;
+        run.to_slot = true;
+        if (++upair == npairs) { upair = 0; ++useq; }
+      } else {                  // the last part of the unit at the range's start
+        run.seq = A.seq; pair = A.pair; run.c0 = A.chunk;
+        run.from_slot = false;
+        run.from_carry = run.to_slot = true;
+        stage = 6;
       }
-      seq = useq; pair = upair; c0 = 0;
-      to_slot = true;
-      if (++upair == npairs) { upair = 0; ++useq; }
-    } else {                  // the last part of the unit at the range's start
-      seq = A.seq; pair = A.pair; c0 = A.chunk;
-      from_slot = false;
-      from_carry = true;
-      to_slot = true;
-      stage = 6;
-    }
-    const int begin = seq_begin(p.seq, seq), end = seq_end(p.seq, seq, begin);
-    if (c1 < 0) c1 = max(1, (end - begin + kQ - 1) / kQ);
-    if (end == begin) c1 = c0;  // nothing to compute, but the state passes through
-    int slot = -1;
-    if (p.state) {
-      slot = claim_slot(p.slots, seq, &g_fault_prefill);
-      if (slot < 0) {
-        if (stage == 1) stage = 6;  // the middle of a skipped sequence
-        continue;
+      run.begin = seq_begin(p.seq, run.seq);
+      run.end = seq_end(p.seq, run.seq, run.begin);
+      if (c1 < 0) c1 = (run.end - run.begin + kQ - 1) / kQ;
+      run.n = c1 - run.c0;  // 0 for an empty sequence: the state passes through
+      run.slot = -1;
+      if (p.state) {
+        run.slot = claim_slot(p.slots, run.seq, &g_fault_prefill);
+        if (run.slot < 0) {
+          if (stage == 1) stage = 6;  // the middle of a skipped sequence
+          continue;
+        }
       }
+      run.g = pair / ppg;
+      run.h0 = run.g * per + 2 * (pair - run.g * ppg);
+      run.nh2 = min(2, run.g * per + per - run.h0);  // an odd group's last pair holds one head
+      return true;
     }
-    const int g = pair / ppg, h0 = g * per + 2 * (pair - g * ppg);
-    const int nh2 = min(2, g * per + per - h0);  // an odd group's last pair holds one head
+    return false;
+  };
+  // The run is done in all warps; false when the block gives up.
+  auto done = [&]() -> bool {
+    it += run.n;
+    if (run.full) itf += run.n;
+    return !__syncthreads_or(!ok);
+  };
 
-    if (warp == kTmaWarp) {
-      // ------------------------------------------------------------ copies
-      if (lane == 0 && c0 < c1) {
-        auto load = [&](int i, uint32_t off, const CUtensorMap* map, int col, int c, int nb) {
-          tc::expect_tx(bar(i), 16384u * nb);
-          for (int b = 0; b < nb; ++b) tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, begin + c * kQ, bar(i));
-          arm(i);
-        };
-        auto load_b = [&](int c, uint32_t k) { load(kBarB + (k & 1), L::kB + (k & 1) * L::kTile, &map_b, g * N, c, N / 64); };
-        auto load_c = [&](int c) { load(kBarC, L::kC, &map_c, g * N, c, N / 64); };
-        auto load_x = [&](int c, uint32_t k) { load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, c, nh2); };
-        auto store_y = [&](int c, uint32_t k) {
-          for (int b = 0; b < nh2; ++b)
-            tc::tma_store_2d(&map_y, (h0 + b) * kP, begin + c * kQ, sb + L::kX + (k & 1) * 32768 + 16384u * b);
-          tc::bulk_commit();
-        };
-        load_b(c0, it);
-        if (full) load_c(c0);
-        load_x(c0, it);
-        for (int c = c0; c < c1 && ok; ++c) {
-          const uint32_t k = it + (c - c0), kf = itf + (c - c0);
-          if (c > c0) {  // the other buffers' last readers, in the chunk before
-            wait(kBarSall, k - 1, 2u);
-            if (full) {
-              wait(kBarY, kf - 1, 2u);
-              if (!ok) break;
-              store_y(c - 1, k - 1);
-            }
-          }
-          if (c + 1 < c1) {
-            load_b(c + 1, k + 1);
-            if (full) tc::bulk_wait_read_all();
-            load_x(c + 1, k + 1);
-            if (full) {
-              wait(kBarYc, kf, 2u);
-              if (!ok) break;
-              load_c(c + 1);
-            }
-          }
-        }
-        const int last = c1 - 1;
-        if (full && ok) {
-          wait(kBarY, itf + (last - c0), 2u);
-          if (ok && begin + (last + 1) * kQ <= end) store_y(last, it + (last - c0));  // a ragged chunk is written below
-        }
-        tc::bulk_wait_read_all();
-      }
-      __syncwarp();
-    } else if (warp == kMmaWarp) {
-      // ---------------------------------------------------------- products
-      if (lane == 0) {
-        for (int c = c0; c < c1 && ok; ++c) {
-          const uint32_t k = it + (c - c0), kf = itf + (c - c0);
-          const uint32_t offB = L::kB + (k & 1) * L::kTile, offX = L::kX + (k & 1) * 32768;
-          wait(kBarB + (k & 1), k >> 1, 1u);
-          if (full) {
-            wait(kBarC, kf, 1u);
-            if (c > c0) wait(kBarY, kf - 1, 2u);  // the accumulators of y are read
-            if (!ok) break;
-            tc::fence_after();
-            const uint64_t dc = tc::desc_sw128(sb + L::kC, 16, 1024), db = tc::desc_sw128(sb + offB, 16, 1024),
-                           dh = tc::desc_sw128(sb + L::kH, 16, 1024);
-#pragma unroll
-            for (int kk = 0; kk < N / 16; ++kk) {
-              const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-              tc::mma(tmem + kG, dc + ko, db + ko, kId, kk > 0);
-            }
-            tc::commit(bar(kBarG));
-            arm(kBarG);
-            wait(kBarH, k, 2u);
-            if (!ok) break;
-            tc::fence_after();
-#pragma unroll
-            for (int kk = 0; kk < N / 16; ++kk) {
-              const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-              tc::mma(tmem + kYc, dc + ko, dh + ko, kId, kk > 0);
-            }
-            tc::commit(bar(kBarYc));
-            arm(kBarYc);
-          } else {
-            wait(kBarH, k, 2u);
-            if (!ok) break;
-          }
-          for (int q = 0; q < 4; ++q) {
-            if (q == 3 && full) {  // the warps finish M before the last quarter of Xw
-              wait(kBarM, kf, 2u);
-              if (!ok) break;
-              tc::fence_after();
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const uint64_t dx = tc::desc_sw128(sb + offX + 16384 * b, 16384, 1024);
-#pragma unroll
-                for (int kk = 0; kk < kQ / 16; ++kk)
-                  tc::mma_ta(tmem + kG + 64 * b, tmem + kM + 64 * b + 8 * kk, dx + kk * (2048 >> 4), kIdYm, kk > 0);
-              }
-              tc::commit(bar(kBarYm));
-              arm(kBarYm);
-            }
-            wait(kBarW, q, 2u);
-            if (!ok) break;
-            tc::fence_after();
-            const uint64_t dbm = tc::desc_sw128(sb + offB + q * 4096, 16384, 1024);
-#pragma unroll
-            for (int s3 = 0; s3 < 3; ++s3) {
-              const uint64_t dw = tc::desc_sw128(sb + L::kW + 8192 * s3, 4096, 1024);
-#pragma unroll
-              for (int kk = 0; kk < 2; ++kk)
-                tc::mma(tmem + kS, dw + kk * (2048 >> 4), dbm + kk * (2048 >> 4), kIdS, (q | s3 | kk) != 0);
-            }
-            tc::commit(bar(kBarS));
-            arm(kBarS);
-          }
-          if (!ok) break;
-          tc::commit(bar(kBarSall));
-          arm(kBarSall);
-        }
-      }
-      __syncwarp();
-    } else {
-      // ----------------------------------------------------- compute warps
+  if (warp < 8) {
+    while (next()) {
+      const int n = run.n, end = run.end, h0 = run.h0, nh2 = run.nh2;
+      const bool full = run.full;
+      // ----------------------------------------------------------- M and y
       const int h = h0 + min(hd, nh2 - 1);
-      const bool mine = hd < nh2, owns = hrow < nh2;
-      const float A2 = p.A[h] * kLog2e, Dh = p.D ? p.D[h] : 0.f, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-      const T* dtg = static_cast<const T*>(p.dt) + h;
-      T dtn = Elt<T>::from_f(0.f);
-      auto fetch_dt = [&](int c) {
-        const int t = begin + c * kQ + row;
-        if (c < c1 && t < end) dtn = dtg[(int64_t)t * p.lddt];
-      };
-      // Delta and the decays of chunk c (thread: head hd, token row)
-      auto decays = [&](int c, Arrays& a) {
-        float d = 0.f;
-        if (begin + c * kQ + row < end && mine) {
-          const float v = Elt<T>::to_f(dtn) + bias;
-          d = p.softplus ? softplus_f(v) : v;
-        }
-        float pre = d * A2, suf = pre;
+      const bool mine = hd < nh2;
+      const float Dh = p.D ? p.D[h] : 0.f;
+      for (int j = 0; full && j < n; ++j) {
+        const uint32_t k = it + j, kf = itf + j;
+        const int t0 = run.t0(j), nval = min(kQ, end - t0);
+        const Arrays& a = arr[k & 1];
+        unsigned char* const xs = sm + L::kX + (k & 1) * 32768 + hd * 16384;
+        wait2(kBarA, k, 2);
+        const float pre = a.pre[hd][row];
+        wait(kBarG, kf, 2);
+        tc::fence_after();
+        // ---- M, row `row`: 32 columns at a time, from the diagonal block to the left
+        float between = pre;  // log2 decay from the end of block i to this row
+#pragma unroll 1
+        for (int i = blk; i >= 0; --i) {
+          float gv[32];
+          tc::ld32x32b_x32(tmem + lane_base + kG + 32 * i, gv);
+          uint32_t mp[16];
+          if (i == blk) {
+            const float4* pr = reinterpret_cast<const float4*>(a.pre[hd] + 32 * i);
+            const float4* dl = reinterpret_cast<const float4*>(a.dl[hd] + 32 * i);
+            const f2_t pre2 = pk2(pre, pre), minus = pk2(-1.f, -1.f);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float u = __shfl_up_sync(0xffffffffu, pre, o), v = __shfl_down_sync(0xffffffffu, suf, o);
-          if (lane >= o) pre += u;
-          if (lane + o < 32) suf += v;
+            for (int u = 0; u < 8; ++u) {
+              const float4 pv = pr[u], dv = dl[u];
+              const f2_t m01 = mul2(mul2(pk2(gv[4 * u], gv[4 * u + 1]), ex2_2(fma2(pk2(pv.x, pv.y), minus, pre2))), pk2(dv.x, dv.y));
+              const f2_t m23 = mul2(mul2(pk2(gv[4 * u + 2], gv[4 * u + 3]), ex2_2(fma2(pk2(pv.z, pv.w), minus, pre2))), pk2(dv.z, dv.w));
+              float m[4] = {lo2(m01), hi2(m01), lo2(m23), hi2(m23)};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (4 * u + e > lane) m[e] = 0.f;
+              mp[2 * u] = Pk<T>::pack(m[0], m[1]);
+              mp[2 * u + 1] = Pk<T>::pack(m[2], m[3]);
+            }
+          } else {
+            const float ei = ex2(between);
+            between += a.tot[hd][i];
+            const f2_t ei2 = pk2(ei, ei);
+            const float4* fj = reinterpret_cast<const float4*>(a.f[hd] + 32 * i);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const float4 fv = fj[u];
+              const f2_t m01 = mul2(pk2(gv[4 * u], gv[4 * u + 1]), mul2(ei2, pk2(fv.x, fv.y)));
+              const f2_t m23 = mul2(pk2(gv[4 * u + 2], gv[4 * u + 3]), mul2(ei2, pk2(fv.z, fv.w)));
+              mp[2 * u] = Pk<T>::pack(lo2(m01), hi2(m01));
+              mp[2 * u + 1] = Pk<T>::pack(lo2(m23), hi2(m23));
+            }
+          }
+          tc::st32x32b_x16(tmem + lane_base + kM + 64 * hd + 16 * i, mp);
         }
-        if (lane == 31) a.tot[hd][blk] = pre;
-        suf = __shfl_down_sync(0xffffffffu, suf, 1);  // the tokens after this one
-        if (lane == 31) suf = 0.f;
-        a.f[hd][row] = ex2(suf) * d;
-        a.pre[hd][row] = pre;
-        a.dl[hd][row] = d;
-      };
+        tc::st_wait();
+        signal(kBarM);
+        // ---- y = (2^cs Yc + Ym + D x) SiLU(z), in place of x
+        const float e = ex2(between);  // from the start of the chunk to this row
+        const f2_t e2 = pk2(e, e), D2 = pk2(Dh, Dh);
+        const int64_t t = t0 + row;
+        const T* zg = p.z && mine && row < nval ? static_cast<const T*>(p.z) + t * p.ldz + h * kP : nullptr;
+        wait2(kBarX, k, 1);
+        wait(kBarYc, kf, 2);
+        wait2(kBarR, k, 2);
+        wait(kBarYm, kf, 2);
+        tc::fence_after();
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          float yc[16], ym[16];
+          tc::ld32x32b_x16_pair(tmem + lane_base + kYc + 64 * hd + 16 * i, tmem + lane_base + kG + 64 * hd + 16 * i, yc, ym);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint4* at = reinterpret_cast<uint4*>(xs + swz(row, 2 * i + u));
+            const uint4 xv = *at;
+            const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
+            float o[8];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const float2 f = Pk<T>::unpack(in[v]);
+              const int at8 = 8 * u + 2 * v;
+              const f2_t r = fma2(D2, pk2(f.x, f.y), fma2(e2, pk2(yc[at8], yc[at8 + 1]), pk2(ym[at8], ym[at8 + 1])));
+              o[2 * v] = lo2(r);
+              o[2 * v + 1] = hi2(r);
+            }
+            if (zg) {
+              float zv[8];
+              if (p.zvec) load8(zg + 16 * i + 8 * u, zv);
+              else
+#pragma unroll
+                for (int v = 0; v < 8; ++v) zv[v] = ldf(zg + 16 * i + 8 * u + v);
+#pragma unroll
+              for (int v = 0; v < 8; ++v) o[v] *= zv[v] * sigmoid_f(zv[v]);
+            }
+            if (mine) *at = pack8<T>(o);
+          }
+        }
+        signal(kBarY + (kf & 1));
+        if (nval < kQ) {  // the rows of a ragged chunk, one by one
+          sync_y();
+#pragma unroll 1
+          for (int i = tid; i < nval * 8 * nh2; i += kGroupY) {
+            const int hh = i / (nval * 8), r = (i >> 3) - hh * nval, cc = i & 7;
+            const uint4 v = *reinterpret_cast<const uint4*>(sm + L::kX + (k & 1) * 32768 + hh * 16384 + swz(r, cc));
+            *reinterpret_cast<uint4*>(static_cast<T*>(p.y) + ((int64_t)(t0 + r) * p.nheads + h0 + hh) * kP + 8 * cc) = v;
+          }
+        }
+      }
+      if (!done()) break;
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsS));
+    while (next()) {
+      const int n = run.n, end = run.end, h0 = run.h0, nh2 = run.nh2;
+      const bool full = run.full;
+      // ----------------------------------------------------- Xw and the state
+      const bool owns = hrow < nh2;
+      const int stid = tid - kGroupY, xh = blk >> 1, xc = 4 * (blk & 1);  // Xw: 32 columns of head xh, lanes over tokens
       auto wait_flag = [&]() {  // the state that the block before publishes
-        if (tid == 0) {
+        if (stid == 0) {
           uint32_t polls = 0, v = 0;
           do {
             asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flags + me - 1) : "memory");
           } while (!v && ++polls < kFlagLimit);
           if (!v) {
-            atomicOr(&g_fault_prefill, 2u);
-            s_abort = 1;
+            s_abort = 2;
             ok = false;
           }
         }
-        return !compute_sync_or(!ok);
+        return !sync_s(!ok);
       };
       const float4* const src = carry + (size_t)(me - 1) * (2 * kP * N / 4);
-
-      fetch_dt(c0);
       // ---- the state entering the run
-      float* st = p.state && owns ? p.state + (((size_t)slot * p.nheads + h0) * kP + row) * N + hd * HN : nullptr;
+      float hs[N];
+      float* st = p.state && owns ? p.state + (((size_t)run.slot * p.nheads + h0) * kP + row) * N : nullptr;
 #pragma unroll
-      for (int i = 0; i < HN; ++i) hs[i] = 0.f;
-      if (from_carry) {
+      for (int i = 0; i < N; ++i) hs[i] = 0.f;
+      if (run.from_carry) {
         if (!middle) wait_flag();  // the middle's first pass has waited already
 #pragma unroll
-        for (int i = 0; i < HN / 4; ++i) {
-          const float4 v = __ldcg(src + i * kCompute + tid);
+        for (int i = 0; i < N / 4; ++i) {
+          const float4 v = __ldcg(src + i * kGroupS + stid);
           hs[4 * i] = v.x; hs[4 * i + 1] = v.y; hs[4 * i + 2] = v.z; hs[4 * i + 3] = v.w;
         }
-      } else if (from_slot && st && !(p.slots.fresh && p.slots.fresh[seq])) {
+      } else if (run.from_slot && st && !(p.slots.fresh && p.slots.fresh[run.seq])) {
 #pragma unroll
-        for (int i = 0; i < HN / 4; ++i) {
-          const float4 v = __ldcs(reinterpret_cast<const float4*>(st) + i);
-          hs[4 * i] = v.x; hs[4 * i + 1] = v.y; hs[4 * i + 2] = v.z; hs[4 * i + 3] = v.w;
-        }
+        for (int i = 0; i < N; i += 8) ld_v8(st + i, hs + i);
       }
       // its 16-bit copy: K-major, row = state row
       auto write_copy = [&]() {
-        const int n0 = hd * HN;
-        unsigned char* base = sm + L::kH + (n0 / 64) * 16384;
 #pragma unroll
-        for (int k = 0; k < HN / 8; ++k)
-          *reinterpret_cast<uint4*>(base + swz(row, (n0 % 64) / 8 + k)) = pack8<T>(hs + 8 * k);
+        for (int q = 0; q < N / 8; ++q)
+          *reinterpret_cast<uint4*>(sm + L::kH + (q / 8) * 16384 + swz(row, q % 8)) = pack8<T>(hs + 8 * q);
       };
-      auto signal = [&](int i) {  // generic and TMEM accesses of the warp, then one arrival
-        tc::fence_proxy_async();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) arrive(bar(i));
-      };
-      if (c0 < c1) {
+      if (n > 0) {
         if (full) write_copy();
         if (nh2 == 1)  // the missing head's x is zero
-          for (int i = tid; i < 2048; i += kCompute)
+#pragma unroll 1
+          for (int i = stid; i < 2048; i += kGroupS)
             *reinterpret_cast<uint4*>(sm + L::kX + (i >> 10) * 32768 + 16384 + 16 * (i & 1023)) = make_uint4(0, 0, 0, 0);
-        decays(c0, arr[it & 1]);
-        fetch_dt(c0 + 1);
-        signal(kBarH);
-        compute_sync_or(false);
+        signal(kBarH + (it & 1));
+        if (nh2 == 1) sync_s(false);
       }
       float psum = 0.f;  // log2 decay of the run so far (head hrow)
 
-      for (int c = c0; c < c1; ++c) {
-        const uint32_t k = it + (c - c0), kf = itf + (c - c0);
-        const int t0 = begin + c * kQ, nval = min(kQ, end - t0);
-        const bool more = c + 1 < c1;
+      for (int j = 0; j < n; ++j) {
+        const uint32_t k = it + j, kf = itf + j;
+        const int nval = min(kQ, end - run.t0(j));
         const Arrays& a = arr[k & 1];
         unsigned char* const xs = sm + L::kX + (k & 1) * 32768;
-        wait(kBarX + (k & 1), k >> 1, 1u);
+        wait2(kBarX, k, 1);
         if (nval < kQ) {  // rows behind the sequence belong to others: no NaN of theirs may meet a zero weight
-          wait(kBarB + (k & 1), k >> 1, 1u);
+          wait2(kBarB, k, 1);
           const uint4 zero = make_uint4(0, 0, 0, 0);
-          for (int i = tid; i < (kQ - nval) * 8; i += kCompute) {
+#pragma unroll 1
+          for (int i = stid; i < (kQ - nval) * 8; i += kGroupS) {
             const uint32_t o = (nval + i / 8) * 128 + (i & 7) * 16;
 #pragma unroll
             for (int b = 0; b < N / 64; ++b) *reinterpret_cast<uint4*>(sm + L::kB + (k & 1) * L::kTile + 16384 * b + o) = zero;
             *reinterpret_cast<uint4*>(xs + o) = zero;
             *reinterpret_cast<uint4*>(xs + 16384 + o) = zero;
           }
-          compute_sync_or(false);
+          sync_s(false);
         }
+        wait2(kBarA, k, 2);
         float scale = 1.f, unscale = 1.f;
-        const int xc = 2 * blk;  // Xw: 16 columns of head hd, lanes over tokens
         if constexpr (!kBf16) {  // fp16: the power of two that puts max (|x| Delta) below 2^15
-          if (tid < 2) sMax[tid] = 0u;
-          compute_sync_or(false);
+          if (stid < 2) sMax[stid] = 0u;
+          sync_s(false);
+#pragma unroll 1
+          for (int e = 0; e < 2; ++e) {
           unsigned m = 0;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 v = *reinterpret_cast<const uint4*>(xs + hd * 16384 + swz(row, j));
+          for (int q = 0; q < 8; ++q) {
+            const uint4 v = *reinterpret_cast<const uint4*>(xs + e * 16384 + swz(row, q));
             m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
           }
           m = max(m & 0xffffu, m >> 16);
-          float top = __half2float(__ushort_as_half((unsigned short)m)) * fabsf(a.dl[hd][row]);
+          float top = __half2float(__ushort_as_half((unsigned short)m)) * fabsf(a.dl[e][row]);
           top = top < 3.0e38f ? top : 1.f;
 #pragma unroll
           for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (lane == 0) atomicMax(sMax + hd, __float_as_uint(top));
-          compute_sync_or(false);
+          if (lane == 0) atomicMax(sMax + e, __float_as_uint(top));
+          }
+          sync_s(false);
           auto power = [](unsigned v) {  // 2^(14 - exponent of v), within fp32's range
             const int e = (int)(v >> 23) - 127;
             return v == 0 ? 0 : min(100, max(-100, 14 - e));
           };
-          scale = __uint_as_float((unsigned)(127 + power(sMax[hd])) << 23);
+          scale = __uint_as_float((unsigned)(127 + power(sMax[xh])) << 23);
           unscale = __uint_as_float((unsigned)(127 - power(sMax[hrow])) << 23);
         }
-        // ---- 32 tokens of Xw as three 16-bit pieces
-        auto write_xw = [&](int q) {
-          float later = 0.f;
-          for (int b = q + 1; b < 4; ++b) later += a.tot[hd][b];
-          const float w = a.f[hd][32 * q + lane] * ex2(later) * scale;
+        // ---- Xw, 32 tokens at a time, as three 16-bit pieces
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float later = 0.f;  // log2 decay of the blocks behind
+          for (int b = q + 1; b < 4; ++b) later += a.tot[xh][b];
+          const float w = a.f[xh][32 * q + lane] * ex2(later) * scale;
           const f2_t w2 = pk2(w, w), minus = pk2(-1.f, -1.f);
-          uint32_t u[8], v[8], z[8];
-#pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
-            const uint4 xv = *reinterpret_cast<const uint4*>(xs + hd * 16384 + swz(32 * q + lane, xc + k2));
+          const unsigned char* const from = xs + xh * 16384;
+          unsigned char* const to = sm + L::kW + xh * 4096;
+          if (q > 0) wait(kBarS, q - 1, 2);  // the products of the quarter before have read the buffer
+#pragma unroll 1
+          for (int k4 = xc; k4 < xc + 4; ++k4) {
+            const uint4 xv = *reinterpret_cast<const uint4*>(from + swz(32 * q + lane, k4));
             const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
+            uint32_t u[4], v[4], z[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 f = Pk<T>::unpack(in[e]);
               const f2_t x0 = mul2(pk2(f.x, f.y), w2);
-              const uint32_t p0 = Pk<T>::pack(lo2(x0), hi2(x0));
-              const float2 f0 = Pk<T>::unpack(p0);
+              u[e] = Pk<T>::pack(lo2(x0), hi2(x0));
+              const float2 f0 = Pk<T>::unpack(u[e]);
               const f2_t x1 = fma2(pk2(f0.x, f0.y), minus, x0);
-              const uint32_t p1 = Pk<T>::pack(lo2(x1), hi2(x1));
-              const float2 f1 = Pk<T>::unpack(p1);
+              v[e] = Pk<T>::pack(lo2(x1), hi2(x1));
+              const float2 f1 = Pk<T>::unpack(v[e]);
               const f2_t x2 = fma2(pk2(f1.x, f1.y), minus, x1);
-              u[4 * k2 + e] = p0;
-              v[4 * k2 + e] = p1;
-              z[4 * k2 + e] = Pk<T>::pack(lo2(x2), hi2(x2));
+              z[e] = Pk<T>::pack(lo2(x2), hi2(x2));
             }
-          }
-          if (q > 0) wait(kBarS, q - 1, 2u);  // the products of the quarter before have read the buffer
-#pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
-            unsigned char* wd = sm + L::kW + hd * 4096 + swz(lane, xc + k2);
-            *reinterpret_cast<uint4*>(wd) = make_uint4(u[4 * k2], u[4 * k2 + 1], u[4 * k2 + 2], u[4 * k2 + 3]);
-            *reinterpret_cast<uint4*>(wd + 8192) = make_uint4(v[4 * k2], v[4 * k2 + 1], v[4 * k2 + 2], v[4 * k2 + 3]);
-            *reinterpret_cast<uint4*>(wd + 16384) = make_uint4(z[4 * k2], z[4 * k2 + 1], z[4 * k2 + 2], z[4 * k2 + 3]);
+            const uint32_t o = swz(lane, k4);
+            *reinterpret_cast<uint4*>(to + o) = make_uint4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<uint4*>(to + 8192 + o) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(to + 16384 + o) = make_uint4(z[0], z[1], z[2], z[3]);
           }
           signal(kBarW);
-        };
-        // ---- columns 32 j .. of M, row `row`, head hd
-        const float pre = a.pre[hd][row];
-        auto write_m = [&](int j) {
-          float gv[32];
-          tc::ld32x32b_x32(tmem + lane_base + kG + 32 * j, gv);
-          uint32_t mp[16];
-          if (j == blk) {
-            const float4* pr = reinterpret_cast<const float4*>(a.pre[hd] + 32 * j);
-            const float4* dl = reinterpret_cast<const float4*>(a.dl[hd] + 32 * j);
-            const f2_t pre2 = pk2(pre, pre), minus = pk2(-1.f, -1.f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 pv = pr[i], dv = dl[i];
-              const f2_t m01 = mul2(mul2(pk2(gv[4 * i], gv[4 * i + 1]), ex2_2(fma2(pk2(pv.x, pv.y), minus, pre2))), pk2(dv.x, dv.y));
-              const f2_t m23 = mul2(mul2(pk2(gv[4 * i + 2], gv[4 * i + 3]), ex2_2(fma2(pk2(pv.z, pv.w), minus, pre2))), pk2(dv.z, dv.w));
-              float m[4] = {lo2(m01), hi2(m01), lo2(m23), hi2(m23)};
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (4 * i + e > lane) m[e] = 0.f;
-              mp[2 * i] = Pk<T>::pack(m[0], m[1]);
-              mp[2 * i + 1] = Pk<T>::pack(m[2], m[3]);
-            }
-          } else {
-            float x = pre;  // from the end of block j to this row
-            for (int b = j + 1; b < blk; ++b) x += a.tot[hd][b];
-            const float ei = ex2(x);
-            const f2_t ei2 = pk2(ei, ei);
-            const float4* fj = reinterpret_cast<const float4*>(a.f[hd] + 32 * j);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 fv = fj[i];
-              const f2_t m01 = mul2(pk2(gv[4 * i], gv[4 * i + 1]), mul2(ei2, pk2(fv.x, fv.y)));
-              const f2_t m23 = mul2(pk2(gv[4 * i + 2], gv[4 * i + 3]), mul2(ei2, pk2(fv.z, fv.w)));
-              mp[2 * i] = Pk<T>::pack(lo2(m01), hi2(m01));
-              mp[2 * i + 1] = Pk<T>::pack(lo2(m23), hi2(m23));
-            }
-          }
-          tc::st32x32b_x16(tmem + lane_base + kM + 64 * hd + 16 * j, mp);
-        };
-        write_xw(0);
-        if (full) {
-          wait(kBarG, kf, 2u);
-          tc::fence_after();
-          write_m(blk);
         }
-        write_xw(1);
-        if (full && blk >= 1) write_m(blk - 1);
-        write_xw(2);
-        if (full) {
-          if (blk >= 2) write_m(blk - 2);
-          if (blk >= 3) write_m(blk - 3);
-          tc::st_wait();
-          signal(kBarM);
-        }
-        write_xw(3);
-        if (more) decays(c + 1, arr[(k + 1) & 1]);
-        fetch_dt(c + 2);
-        // ---- y = (2^cs Yc + Ym + D x) SiLU(z), in place of x
-        if (full) {
-          float cs = pre;
-          for (int b = 0; b < blk; ++b) cs += a.tot[hd][b];
-          const float e = ex2(cs);
-          const f2_t e2 = pk2(e, e), D2 = pk2(Dh, Dh);
-          const int64_t t = t0 + row;
-          const T* zg = p.z && mine && row < nval ? static_cast<const T*>(p.z) + t * p.ldz + h * kP : nullptr;
-          wait(kBarYc, kf, 2u);
-          wait(kBarYm, kf, 2u);
-          wait(kBarW, 3, 2u);  // every warp has read its x
-          tc::fence_after();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float yc[16], ym[16];
-            tc::ld32x32b_x16(tmem + lane_base + kYc + 64 * hd + 16 * i, yc);
-            tc::ld32x32b_x16(tmem + lane_base + kG + 64 * hd + 16 * i, ym);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint4* at = reinterpret_cast<uint4*>(xs + hd * 16384 + swz(row, 2 * i + u));
-              const uint4 xv = *at;
-              const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
-              float o[8];
-#pragma unroll
-              for (int v = 0; v < 4; ++v) {
-                const float2 f = Pk<T>::unpack(in[v]);
-                const int at8 = 8 * u + 2 * v;
-                const f2_t r = fma2(D2, pk2(f.x, f.y), fma2(e2, pk2(yc[at8], yc[at8 + 1]), pk2(ym[at8], ym[at8 + 1])));
-                o[2 * v] = lo2(r);
-                o[2 * v + 1] = hi2(r);
-              }
-              if (zg) {
-                float zv[8];
-                if (p.zvec) load8(zg + 16 * i + 8 * u, zv);
-                else
-#pragma unroll
-                  for (int v = 0; v < 8; ++v) zv[v] = ldf(zg + 16 * i + 8 * u + v);
-#pragma unroll
-                for (int v = 0; v < 8; ++v) o[v] *= zv[v] * sigmoid_f(zv[v]);
-              }
-              if (mine) *at = pack8<T>(o);
-            }
-          }
-          signal(kBarY);
-          if (nval < kQ) {  // the rows of a ragged chunk, one by one
-            compute_sync_or(false);
-            for (int i = tid; i < nval * 8 * nh2; i += kCompute) {
-              const int hh = i / (nval * 8), r = (i >> 3) - hh * nval, cc = i & 7;
-              const uint4 v = *reinterpret_cast<const uint4*>(xs + hh * 16384 + swz(r, cc));
-              *reinterpret_cast<uint4*>(static_cast<T*>(p.y) + ((int64_t)(t0 + r) * p.nheads + h0 + hh) * kP + 8 * cc) = v;
-            }
-          }
-        }
+        if (lane == 0) arrive(bar(kBarR + (k & 1)));  // (the signal above ordered the warp's accesses)
         // ---- H <- 2^cs_last H + S
-        wait(kBarSall, k, 2u);
+        const float tot = (a.tot[hrow][0] + a.tot[hrow][1]) + (a.tot[hrow][2] + a.tot[hrow][3]);
+        psum += tot;
+        const float dec = ex2(tot);
+        if (full) wait(kBarYc, kf, 2);  // C H^T is done with the state copy
+        wait(kBarS, 3, 2);
         tc::fence_after();
-        {
-          const float tot = (a.tot[hrow][0] + a.tot[hrow][1]) + (a.tot[hrow][2] + a.tot[hrow][3]);
-          psum += tot;
-          const float dec = ex2(tot);
+        const f2_t dec2 = pk2(dec, dec), un2 = pk2(unscale, unscale);
 #pragma unroll
-          for (int n = 0; n < HN; n += 16) {
-            float sv[16];
-            tc::ld32x32b_x16(tmem + lane_base + kS + hd * HN + n, sv);
+        for (int q = 0; q < N; q += 16) {
+          float sv[16];
+          tc::ld32x32b_x16(tmem + lane_base + kS + q, sv);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) hs[n + i] = fmaf(dec, hs[n + i], kBf16 ? sv[i] : sv[i] * unscale);
+          for (int i = 0; i < 16; i += 2) {
+            f2_t v = pk2(sv[i], sv[i + 1]);
+            if (!kBf16) v = mul2(v, un2);
+            v = fma2(dec2, pk2(hs[q + i], hs[q + i + 1]), v);
+            hs[q + i] = lo2(v);
+            hs[q + i + 1] = hi2(v);
           }
         }
-        if (more) {
-          if (full) write_copy();  // C H^T of this chunk is done with the old copy
-          signal(kBarH);
-        }
-        if (compute_sync_or(!ok)) {
-          ok = false;
-          break;
+        if (j + 1 < n) {
+          if (full) write_copy();
+          signal(kBarH + ((k + 1) & 1));
         }
       }
+      ok = !sync_s(!ok);
 
       // ---- the state leaving the run
-      if (!full && ok) {  // the middle of a unit: add what enters it, decayed
-        if (wait_flag()) {
-          const float dec = ex2(psum);
+      if (!full && ok && wait_flag()) {  // the middle of a unit: add what enters it, decayed
+        const float dec = ex2(psum);
 #pragma unroll
-          for (int i = 0; i < HN / 4; ++i) {
-            const float4 v = __ldcg(src + i * kCompute + tid);
-            hs[4 * i] = fmaf(dec, v.x, hs[4 * i]);
-            hs[4 * i + 1] = fmaf(dec, v.y, hs[4 * i + 1]);
-            hs[4 * i + 2] = fmaf(dec, v.z, hs[4 * i + 2]);
-            hs[4 * i + 3] = fmaf(dec, v.w, hs[4 * i + 3]);
+        for (int i = 0; i < N / 4; ++i) {
+          const float4 v = __ldcg(src + i * kGroupS + stid);
+          hs[4 * i] = fmaf(dec, v.x, hs[4 * i]);
+          hs[4 * i + 1] = fmaf(dec, v.y, hs[4 * i + 1]);
+          hs[4 * i + 2] = fmaf(dec, v.z, hs[4 * i + 2]);
+          hs[4 * i + 3] = fmaf(dec, v.w, hs[4 * i + 3]);
+        }
+      }
+      if (run.publish) {
+        float4* dst = carry + (size_t)me * (2 * kP * N / 4);
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+          dst[i * kGroupS + stid] = make_float4(hs[4 * i], hs[4 * i + 1], hs[4 * i + 2], hs[4 * i + 3]);
+        __threadfence();
+        sync_s(false);
+        if (stid == 0) asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(flags + me) : "memory");
+      } else if (run.to_slot && st) {
+#pragma unroll
+        for (int i = 0; i < N; i += 8) st_v8(st + i, hs + i);
+      }
+      if (!done()) break;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsHelp));
+  if (warp == kTmaWarp) {
+    while (next()) {
+      const int n = run.n, c0 = run.c0, c1 = c0 + n, end = run.end, h0 = run.h0, nh2 = run.nh2;
+      const bool full = run.full;
+      // ------------------------------------------------------------ copies
+      if (lane == 0 && n > 0) {
+        auto load = [&](int i, uint32_t off, const CUtensorMap* map, int col, int c, int nb) {
+          tc::expect_tx(bar(i), 16384u * nb);
+          for (int b = 0; b < nb; ++b) tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, run.begin + c * kQ, bar(i));
+          arm(i);
+        };
+        auto load_b = [&](int c, uint32_t k) { load(kBarB + (k & 1), L::kB + (k & 1) * L::kTile, &map_b, run.g * N, c, N / 64); };
+        auto load_c = [&](int c) { load(kBarC, L::kC, &map_c, run.g * N, c, N / 64); };
+        auto load_x = [&](int c, uint32_t k) { load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, c, nh2); };
+        auto store_y = [&](int c, uint32_t k) {
+          for (int b = 0; b < nh2; ++b)
+            tc::tma_store_2d(&map_y, (h0 + b) * kP, run.begin + c * kQ, sb + L::kX + (k & 1) * 32768 + 16384u * b);
+          tc::bulk_commit();
+        };
+        load_x(c0, it);
+        load_b(c0, it);
+        if (full) load_c(c0);
+        for (int j = 0; j < n && ok; ++j) {
+          const int c = c0 + j;
+          const uint32_t k = it + j, kf = itf + j;
+          if (j > 0) {  // the other buffers' last readers, in the chunk before
+            wait2(kBarSall, k - 1, 2);
+            if (full) wait2(kBarY, kf - 1, 2);
+            if (!ok) break;
+            if (full) store_y(c - 1, k - 1);
+          }
+          if (j + 1 < n) {
+            load_b(c + 1, k + 1);  // G of the chunk before was done before its C went
+            if (full) tc::bulk_wait_read_all();
+            load_x(c + 1, k + 1);
+            if (full) {
+              wait(kBarYc, kf, 2);
+              if (!ok) break;
+              load_c(c + 1);
+            }
+          }
+        }
+        if (full && ok) {
+          wait2(kBarY, itf + n - 1, 2);
+          if (ok && run.t0(n) <= end) store_y(c1 - 1, it + n - 1);  // a ragged chunk is written by the y group
+        }
+        tc::bulk_wait_read_all();
+      }
+      __syncwarp();
+      if (!done()) break;
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ products
+    // One warp issues them all.  It follows two sequences, the products of y and
+    // those of the state, and issues the next batch of whichever is ready.  The
+    // issuing lane is picked by elect.sync: in a branch on the thread number
+    // the compiler cannot take descriptors for uniform, and a product of
+    // 128 x 128 x 16 takes 170-220 cycles to issue instead of 66 to execute.
+    while (next()) {
+      const int n = run.n, end = run.end;
+      {
+        auto ready = [&](int i, uint32_t parity) { return tc::test(bar(i), parity & 1u); };
+        auto ready2 = [&](int i, uint32_t k) { return ready(i + (int)(k & 1), k >> 1); };
+        int jy = run.full ? 0 : n, js = 0, sy = 0, q = 0;  // chunk and step of either sequence
+        uint32_t idle = 0;
+        while (ok && (jy < n || js < n)) {
+          bool issued = false;
+          if (js < n) {
+            const uint32_t k = it + js;
+            if (ready(kBarW, q) && ready2(kBarB, k) && ready2(kBarH, k)) {
+              tc::fence_after();
+              if (tc::elect()) {
+                const uint64_t dbm = tc::desc_sw128(sb + L::kB + (k & 1) * L::kTile + q * 4096, 16384, 1024);
+                const uint64_t dw = tc::desc_sw128(sb + L::kW, 4096, 1024);
+#pragma unroll 1
+                for (int i = 0; i < 6; ++i)  // three pieces, two steps of 16 tokens
+                  tc::mma(tmem + kS, dw + ((i >> 1) * 8192 + (i & 1) * 2048) / 16, dbm + (i & 1) * (2048 >> 4), kIdS,
+                          (q | i) != 0);
+                tc::commit(bar(kBarS));
+                if (q == 3) tc::commit(bar(kBarSall + (k & 1)));
+              }
+              __syncwarp();
+              arm(kBarS);
+              if (q == 3) {
+                arm(kBarSall + (k & 1));
+                ++js;
+              }
+              q = (q + 1) & 3;
+              issued = true;
+            }
+          }
+          if (jy < n) {
+            const uint32_t k = it + jy, kf = itf + jy;
+            if (sy < 2) {
+              const bool go = sy == 0 ? ready2(kBarB, k) && ready(kBarC, kf) && (jy == 0 || ready2(kBarY, kf - 1))
+                                      : ready2(kBarH, k);
+              if (go) {  // G = C B^T; Yc = C H^T
+                tc::fence_after();
+                const int b = sy == 0 ? kBarG : kBarYc;
+                if (tc::elect()) {
+                  const uint64_t dc = tc::desc_sw128(sb + L::kC, 16, 1024);
+                  const uint64_t db = tc::desc_sw128(sb + (sy == 0 ? L::kB + (k & 1) * L::kTile : L::kH), 16, 1024);
+                  const uint32_t to = tmem + (sy == 0 ? kG : kYc);
+#pragma unroll 1
+                  for (int kk = 0; kk < N / 16; ++kk) {
+                    const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                    tc::mma(to, dc + ko, db + ko, kId, kk > 0);
+                  }
+                  tc::commit(bar(b));
+                }
+                __syncwarp();
+                arm(b);
+                ++sy;
+                issued = true;
+              }
+            } else if (ready(kBarM, kf) && ready2(kBarX, k) && (run.t0(jy + 1) <= end || ready2(kBarR, k))) {
+              tc::fence_after();  // (a ragged chunk's x is cleared behind its end before kBarR)
+              if (tc::elect()) {
+                const uint64_t dx = tc::desc_sw128(sb + L::kX + (k & 1) * 32768, 16384, 1024);
+#pragma unroll 1
+                for (int i = 0; i < 16; ++i)  // two heads, 8 steps of 16 tokens; the second head's x is 16 KB on
+                  tc::mma_ta(tmem + kG + 64 * (i >> 3), tmem + kM + 8 * i, dx + i * (2048 >> 4), kIdYm, (i & 7) != 0);
+                tc::commit(bar(kBarYm));
+              }
+              __syncwarp();
+              arm(kBarYm);
+              sy = 0;
+              ++jy;
+              issued = true;
+            }
+          }
+          if (issued) {
+            idle = 0;
+          } else {
+            if (++idle == kWaitLimit * 8) s_abort = 2;
+            if (*reinterpret_cast<volatile int*>(&s_abort)) ok = false;
           }
         }
       }
-      if (publish) {
-        float4* dst = carry + (size_t)me * (2 * kP * N / 4);
-#pragma unroll
-        for (int i = 0; i < HN / 4; ++i)
-          dst[i * kCompute + tid] = make_float4(hs[4 * i], hs[4 * i + 1], hs[4 * i + 2], hs[4 * i + 3]);
-        __threadfence();
-        compute_sync_or(false);
-        if (tid == 0) asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(flags + me) : "memory");
-      } else if (to_slot && st) {
-#pragma unroll
-        for (int i = 0; i < HN / 4; ++i)
-          __stcs(reinterpret_cast<float4*>(st) + i, make_float4(hs[4 * i], hs[4 * i + 1], hs[4 * i + 2], hs[4 * i + 3]));
-      }
+      __syncwarp();
+      if (!done()) break;
     }
-    it += c1 - c0;
-    if (full) itf += c1 - c0;
-    if (__syncthreads_or(!ok)) break;
+  } else {
+    // ------------------------- Delta and the decays of a head, a chunk ahead
+    const int e = warp - kDecayWarp;
+    while (next()) {
+      const int n = run.n, end = run.end, h = run.h0 + min(e, run.nh2 - 1);
+      const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+      const T* const dtg = static_cast<const T*>(p.dt) + h;
+      const bool have = e < run.nh2;
+      float dtn[4];  // token 32 b + lane
+      auto fetch = [&](int j) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int t = run.t0(j) + 32 * b + lane;
+          dtn[b] = j < n && t < end ? Elt<T>::to_f(dtg[(int64_t)t * p.lddt]) : 0.f;
+        }
+      };
+      fetch(0);
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        const uint32_t k = it + j;
+        float d[4], pre[4], suf[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const float v = dtn[b] + bias;
+          d[b] = p.softplus ? softplus_f(v) : v;
+          if (run.t0(j) + 32 * b + lane >= end || !have) d[b] = 0.f;
+          pre[b] = suf[b] = d[b] * A2;
+        }
+        fetch(j + 1);
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const float u = __shfl_up_sync(0xffffffffu, pre[b], o), v = __shfl_down_sync(0xffffffffu, suf[b], o);
+            if (lane >= o) pre[b] += u;
+            if (lane + o < 32) suf[b] += v;
+          }
+        // the readers of this buffer, two chunks before
+        if (j > 1) wait2(kBarH, k - 1, 2);
+        if (j > 1 && run.full) wait2(kBarY, itf + j - 2, 2);
+        Arrays& a = arr[k & 1];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int r = 32 * b + lane;
+          float after = __shfl_down_sync(0xffffffffu, suf[b], 1);  // the tokens after this one
+          if (lane == 31) {
+            a.tot[e][b] = pre[b];
+            after = 0.f;
+          }
+          a.f[e][r] = ex2(after) * d[b];
+          a.pre[e][r] = pre[b];
+          a.dl[e][r] = d[b];
+        }
+        __syncwarp();
+        if (lane == 0) arrive(bar(kBarA + (k & 1)));
+      }
+      if (!done()) break;
+    }
+  }
   }
 
   // Drain: copies and products in flight must be done before shared memory and
   // TMEM are given back (a no-op on the normal path, but for the last y).
-  if (lane == 0 && warp >= 8) {
+  if (lane == 0 && warp >= 12) {
 #pragma unroll
-    for (int i = 0; i < kBarW; ++i)
+    for (int i = 0; i < kNumTx; ++i)
       if ((armed >> i) & 1u)
         if (!tc::wait(bar(i), (last_par >> i) & 1u, kWaitLimit)) atomicOr(&g_fault_prefill, 4u);
     tc::bulk_wait_all();
   }
   tc::fence_before();
   __syncthreads();
+  if (tid == 0 && s_abort) atomicOr(&g_fault_prefill, (unsigned)s_abort);
   if (warp == 0) {
     tc::fence_after();
     tc::tmem_dealloc(tmem, 512);
