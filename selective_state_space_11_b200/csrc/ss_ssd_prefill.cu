@@ -162,15 +162,15 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const SsdPrefillPara
 template <int N>
 struct Lay {
   static constexpr int kTile = N * 256;               // 128 rows x N 16-bit
-  static constexpr int kB = 0;                        // two of them
-  static constexpr int kC = 2 * kTile;
+  static constexpr int kB = 0;
+  static constexpr int kC = kTile;
   static constexpr int kX = kC + kTile;               // two of 2 heads x 128 rows x 128 B: x, then y in its place
-  static constexpr int kW = kX + 65536;               // 3 pieces x 2 heads x 32 rows x 128 B
-  static constexpr int kH = kW + 24576;               // 128 rows x N 16-bit
+  static constexpr int kW = kX + 65536;               // two of 3 pieces x 2 heads x 32 rows x 128 B
+  static constexpr int kH = kW + 2 * 24576;           // 128 rows x N 16-bit
   static constexpr int kArr = kH + kTile;             // two of Arrays
   static constexpr int kMax = kArr + 2 * 3104;        // unsigned [2]: largest |x| Delta of the chunk (fp16)
   static constexpr int kBars = kMax + 16;             // mbarriers
-  static constexpr int kSlot = kBars + 176;  // TMEM base address
+  static constexpr int kSlot = kBars + 176;  // TMEM base address  // TMEM base address
   static constexpr int kBytes = kSlot + 16;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -186,25 +186,25 @@ static_assert(sizeof(Arrays) == 3104, "Lay::kMax");
 // A parity names a phase only to a thread that can be neither a phase behind
 // nor one ahead.  The pairs [2] alternate between chunks (or chunks in full,
 // for those of y), because their waiters and the next chunk's signallers are
-// not ordered more tightly; kBarS and kBarW have four phases per chunk, each of
-// which is waited for; the others have one per chunk in full.
+// not ordered more tightly; kBarS and kBarW alternate between the quarters of
+// a chunk, two phases each; the others have one phase per chunk (in full).
 enum : int {
-  kBarB = 0,      // [2]
-  kBarX = 2,      // [2]
-  kBarSall = 4,   // [2] all of S (for the copies)
-  kBarC = 6,
-  kBarG = 7,      // G
-  kBarYc = 8,     // C H^T
-  kBarYm = 9,     // M X
-  kBarS = 10,     // a quarter of S is done, and with its Xw
+  kBarX = 0,      // [2]
+  kBarSall = 2,   // [2] all of S (for the copies)
+  kBarS = 4,      // [2] a quarter of S is done, and with its Xw
+  kBarB = 6,
+  kBarC = 7,
+  kBarG = 8,      // G
+  kBarYc = 9,     // C H^T
+  kBarYm = 10,    // M X
   kNumTx = 11,    // those above are armed by the copy and product threads
   kBarA = 11,     // [2] the decays are written
-  kBarW = 13,     // a quarter of Xw is written
-  kBarM = 14,     // M is written
-  kBarR = 15,     // [2] Xw's warps are done with x
-  kBarH = 17,     // [2] the state copy is written and S is read: the next chunk's products may start
-  kBarY = 19,     // [2] y is in place of x, its accumulators are read
-  kNumBars = 21
+  kBarW = 13,     // [2] a quarter of Xw is written
+  kBarM = 15,     // M is written
+  kBarR = 16,     // [2] Xw's warps are done with x
+  kBarH = 18,     // [2] the state copy is written and S is read: the next chunk's products may start
+  kBarY = 20,     // [2] y is in place of x, its accumulators are read
+  kNumBars = 22
 };
 
 __device__ __forceinline__ uint32_t swz(int r, int c) {
@@ -598,13 +598,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned char* const xs = sm + L::kX + (k & 1) * 32768;
         wait2(kBarX, k, 1);
         if (nval < kQ) {  // rows behind the sequence belong to others: no NaN of theirs may meet a zero weight
-          wait2(kBarB, k, 1);
+          wait(kBarB, k, 1);
           const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
           for (int i = stid; i < (kQ - nval) * 8; i += kGroupS) {
             const uint32_t o = (nval + i / 8) * 128 + (i & 7) * 16;
 #pragma unroll
-            for (int b = 0; b < N / 64; ++b) *reinterpret_cast<uint4*>(sm + L::kB + (k & 1) * L::kTile + 16384 * b + o) = zero;
+            for (int b = 0; b < N / 64; ++b) *reinterpret_cast<uint4*>(sm + L::kB + 16384 * b + o) = zero;
             *reinterpret_cast<uint4*>(xs + o) = zero;
             *reinterpret_cast<uint4*>(xs + 16384 + o) = zero;
           }
@@ -646,8 +646,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float w = a.f[xh][32 * q + lane] * ex2(later) * scale;
           const f2_t w2 = pk2(w, w), minus = pk2(-1.f, -1.f);
           const unsigned char* const from = xs + xh * 16384;
-          unsigned char* const to = sm + L::kW + xh * 4096;
-          if (q > 0) wait(kBarS, q - 1, 2);  // the products of the quarter before have read the buffer
+          unsigned char* const to = sm + L::kW + (q & 1) * 24576 + xh * 4096;
+          if (q > 1) wait(kBarS + (q & 1), 0, 2);  // the products of the quarter before the last have read the buffer
 #pragma unroll 1
           for (int k4 = xc; k4 < xc + 4; ++k4) {
             const uint4 xv = *reinterpret_cast<const uint4*>(from + swz(32 * q + lane, k4));
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(to + 8192 + o) = make_uint4(v[0], v[1], v[2], v[3]);
             *reinterpret_cast<uint4*>(to + 16384 + o) = make_uint4(z[0], z[1], z[2], z[3]);
           }
-          signal(kBarW);
+          signal(kBarW + (q & 1));
         }
         if (lane == 0) arrive(bar(kBarR + (k & 1)));  // (the signal above ordered the warp's accesses)
         // ---- H <- 2^cs_last H + S
@@ -678,26 +678,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         psum += tot;
         const float dec = ex2(tot);
         if (full) wait(kBarYc, kf, 2);  // C H^T is done with the state copy
-        wait(kBarS, 3, 2);
+        wait(kBarS + 1, 1, 2);
         tc::fence_after();
         const f2_t dec2 = pk2(dec, dec), un2 = pk2(unscale, unscale);
+        const bool more = j + 1 < n;
 #pragma unroll
-        for (int q = 0; q < N; q += 16) {
-          float sv[16];
-          tc::ld32x32b_x16(tmem + lane_base + kS + q, sv);
+        for (int q = 0; q < N; q += 32) {  // with the next chunk's 16-bit copy
+          float sv[32];
+          tc::ld32x32b_x32(tmem + lane_base + kS + q, sv);
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
+          for (int i = 0; i < 32; i += 2) {
             f2_t v = pk2(sv[i], sv[i + 1]);
             if (!kBf16) v = mul2(v, un2);
             v = fma2(dec2, pk2(hs[q + i], hs[q + i + 1]), v);
             hs[q + i] = lo2(v);
             hs[q + i + 1] = hi2(v);
           }
+          if (more && full)
+#pragma unroll
+            for (int i = q / 8; i < q / 8 + 4; ++i)
+              *reinterpret_cast<uint4*>(sm + L::kH + (i / 8) * 16384 + swz(row, i % 8)) = pack8<T>(hs + 8 * i);
         }
-        if (j + 1 < n) {
-          if (full) write_copy();
-          signal(kBarH + ((k + 1) & 1));
-        }
+        if (more) signal(kBarH + ((k + 1) & 1));
       }
       ok = !sync_s(!ok);
 
@@ -740,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int b = 0; b < nb; ++b) tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, run.begin + c * kQ, bar(i));
           arm(i);
         };
-        auto load_b = [&](int c, uint32_t k) { load(kBarB + (k & 1), L::kB + (k & 1) * L::kTile, &map_b, run.g * N, c, N / 64); };
+        auto load_b = [&](int c) { load(kBarB, L::kB, &map_b, run.g * N, c, N / 64); };
         auto load_c = [&](int c) { load(kBarC, L::kC, &map_c, run.g * N, c, N / 64); };
         auto load_x = [&](int c, uint32_t k) { load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, c, nh2); };
         auto store_y = [&](int c, uint32_t k) {
@@ -749,27 +751,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::bulk_commit();
         };
         load_x(c0, it);
-        load_b(c0, it);
+        load_b(c0);
         if (full) load_c(c0);
-        for (int j = 0; j < n && ok; ++j) {
+        for (int j = 0; j < n && ok; ++j) {  // each buffer is loaded again as its last reader is done
           const int c = c0 + j;
           const uint32_t k = it + j, kf = itf + j;
-          if (j > 0) {  // the other buffers' last readers, in the chunk before
-            wait2(kBarSall, k - 1, 2);
-            if (full) wait2(kBarY, kf - 1, 2);
+          if (j > 0 && full) {
+            wait2(kBarY, kf - 1, 2);
             if (!ok) break;
-            if (full) store_y(c - 1, k - 1);
+            store_y(c - 1, k - 1);
           }
-          if (j + 1 < n) {
-            load_b(c + 1, k + 1);  // G of the chunk before was done before its C went
-            if (full) tc::bulk_wait_read_all();
-            load_x(c + 1, k + 1);
-            if (full) {
-              wait(kBarYc, kf, 2);
-              if (!ok) break;
-              load_c(c + 1);
-            }
+          if (j + 1 == n) break;
+          if (full) tc::bulk_wait_read_all();
+          load_x(c + 1, k + 1);
+          if (full) {
+            wait(kBarYc, kf, 2);
+            if (!ok) break;
+            load_c(c + 1);
           }
+          wait2(kBarSall, k, 2);
+          if (ok) load_b(c + 1);
         }
         if (full && ok) {
           wait2(kBarY, itf + n - 1, 2);
@@ -798,20 +799,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool issued = false;
           if (js < n) {
             const uint32_t k = it + js;
-            if (ready(kBarW, q) && ready2(kBarB, k) && ready2(kBarH, k)) {
+            if (ready(kBarW + (q & 1), q >> 1) && ready(kBarB, k) && ready2(kBarH, k)) {
               tc::fence_after();
               if (tc::elect()) {
-                const uint64_t dbm = tc::desc_sw128(sb + L::kB + (k & 1) * L::kTile + q * 4096, 16384, 1024);
-                const uint64_t dw = tc::desc_sw128(sb + L::kW, 4096, 1024);
+                const uint64_t dbm = tc::desc_sw128(sb + L::kB + q * 4096, 16384, 1024);
+                const uint64_t dw = tc::desc_sw128(sb + L::kW + (q & 1) * 24576, 4096, 1024);
 #pragma unroll 1
                 for (int i = 0; i < 6; ++i)  // three pieces, two steps of 16 tokens
                   tc::mma(tmem + kS, dw + ((i >> 1) * 8192 + (i & 1) * 2048) / 16, dbm + (i & 1) * (2048 >> 4), kIdS,
                           (q | i) != 0);
-                tc::commit(bar(kBarS));
+                tc::commit(bar(kBarS + (q & 1)));
                 if (q == 3) tc::commit(bar(kBarSall + (k & 1)));
               }
               __syncwarp();
-              arm(kBarS);
+              arm(kBarS + (q & 1));
               if (q == 3) {
                 arm(kBarSall + (k & 1));
                 ++js;
@@ -823,14 +824,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (jy < n) {
             const uint32_t k = it + jy, kf = itf + jy;
             if (sy < 2) {
-              const bool go = sy == 0 ? ready2(kBarB, k) && ready(kBarC, kf) && (jy == 0 || ready2(kBarY, kf - 1))
+              const bool go = sy == 0 ? ready(kBarB, k) && ready(kBarC, kf) && (jy == 0 || ready2(kBarY, kf - 1))
                                       : ready2(kBarH, k);
               if (go) {  // G = C B^T; Yc = C H^T
                 tc::fence_after();
                 const int b = sy == 0 ? kBarG : kBarYc;
                 if (tc::elect()) {
                   const uint64_t dc = tc::desc_sw128(sb + L::kC, 16, 1024);
-                  const uint64_t db = tc::desc_sw128(sb + (sy == 0 ? L::kB + (k & 1) * L::kTile : L::kH), 16, 1024);
+                  const uint64_t db = tc::desc_sw128(sb + (sy == 0 ? L::kB : L::kH), 16, 1024);
                   const uint32_t to = tmem + (sy == 0 ? kG : kYc);
 #pragma unroll 1
                   for (int kk = 0; kk < N / 16; ++kk) {
