@@ -78,4 +78,19 @@ __device__ __forceinline__ int claim_slot(const Slots& s, int i, unsigned* fault
   return slot < 0 ? -1 : slot;
 }
 
+// The same for the lanes of one warp.
+__device__ __forceinline__ int claim_slot_warp(const Slots& s, int i, unsigned* fault) {
+  if (!s.index) return i;
+  const int slot = s.index[i];
+  bool bad = slot >= s.count;
+  if (slot >= 0 && !bad)
+#pragma unroll 1
+    for (int j = threadIdx.x & 31; j < i; j += 32) bad |= s.index[j] == slot;
+  if (__any_sync(0xffffffffu, bad)) {
+    if ((threadIdx.x & 31) == 0) atomicOr(fault, 8u);
+    return -1;
+  }
+  return slot < 0 ? -1 : slot;
+}
+
 }  // namespace ss

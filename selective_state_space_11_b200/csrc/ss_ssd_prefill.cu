@@ -67,13 +67,14 @@ namespace {
 
 constexpr int kP = 64;         // head dimension
 constexpr int kQ = 128;        // chunk length
-// Warps: 0-7 form M and y (a warpgroup per head), 8-11 Xw and the state, then
-// one for the products, one for the copies and one per head for the decays.  The registers of a block, 128 per thread at launch, are split
+// Warps: 0-7 form M and y (a warpgroup per head), 8-11 hold the state, 12-15
+// form the decays and Xw, then one for the products of y, one for those of the
+// state, one for the copies, and one that finds the block's next run.  The registers of a block, 96 per thread at launch, are split
 // unevenly: the state's warps hold a whole state row each.
-constexpr int kGroupY = 256, kGroupS = 128;  // threads of the two groups
-constexpr int kMmaWarp = 12, kTmaWarp = 13, kDecayWarp = 14;  // and 15
-constexpr int kThreads = 512;
-constexpr int kRegsS = 200, kRegsHelp = 56;  // 2 x 128 + 200 + 56 = 4 x 128 per quarter of the SM
+constexpr int kGroupY = 256, kGroupS = 128;  // threads of the y group, of the state's and Xw's
+constexpr int kMmaY = 16, kMmaS = 17, kTmaWarp = 18, kPlanWarp = 19;
+constexpr int kThreads = 640;
+constexpr int kRegsS = 168, kRegsX = 72, kRegsHelp = 48;  // 2 x 96 + 168 + 72 + 48 = 5 x 96 per quarter of the SM
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr uint32_t kFlagLimit = 1u << 22;  // polls of a predecessor's flag
 constexpr uint32_t kG = 0, kYc = 128, kM = 256, kS = 384;  // TMEM columns (Ym over G)
@@ -169,7 +170,8 @@ struct Lay {
   static constexpr int kH = kW + 2 * 24576;           // 128 rows x N 16-bit
   static constexpr int kArr = kH + kTile;             // two of Arrays
   static constexpr int kMax = kArr + 2 * 3104;        // unsigned [2]: largest |x| Delta of the chunk (fp16)
-  static constexpr int kBars = kMax + 16;             // mbarriers
+  static constexpr int kUn = kMax + 16;               // float [2][2]: 1 / the power of two of Xw (fp16), by chunk and head
+  static constexpr int kBars = kUn + 16;              // mbarriers
   static constexpr int kSlot = kBars + 176;  // TMEM base address  // TMEM base address
   static constexpr int kBytes = kSlot + 16;
   static constexpr int kAlloc = kBytes + 1024;
@@ -213,12 +215,14 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-// Barriers of the y group and of the state group; the latter is true everywhere if any thread's flag is set.
+// Barriers of the y group, of Xw's warps and of the state's; the last is true
+// everywhere if any thread's flag is set.
 __device__ __forceinline__ void sync_y() { asm volatile("barrier.cta.sync 1, 256;\n" ::: "memory"); }
+__device__ __forceinline__ void sync_x() { asm volatile("barrier.cta.sync 2, 128;\n" ::: "memory"); }
 __device__ __forceinline__ bool sync_s(bool v) {
   int r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 2, 128, p;\n selp.b32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 3, 128, p;\n selp.b32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
       : "r"((int)v)
       : "memory");
@@ -261,6 +265,88 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
   return make_uint4(Pk<T>::pack(f[0], f[1]), Pk<T>::pack(f[2], f[3]), Pk<T>::pack(f[4], f[5]), Pk<T>::pack(f[6], f[7]));
 }
 
+// A run of a block: a unit, its chunks [c0, c0 + n), where its state comes from
+// and goes to.  n < 0: there are no more.
+struct Run {
+  int seq, c0, n, begin, end, slot, g, h0, nh2;
+  bool full, from_slot, from_carry, awaited, publish, to_slot;
+  __device__ __forceinline__ int t0(int j) const { return begin + (c0 + j) * kQ; }
+};
+
+// Finds the runs of a block one after the other (all lanes of a warp in step).
+struct Runs {
+  Cut A, E;
+  int stage, useq, upair, npairs, per, ppg;
+  bool same;
+
+  __device__ __forceinline__ void start(const SsdPrefillParams& p, const Cut* cuts, int npairs_) {
+    A = cuts[0];
+    E = cuts[1];
+    npairs = npairs_;
+    per = p.nheads / p.ngroups;
+    ppg = (per + 1) / 2;  // heads and pairs per group
+    same = A.seq == E.seq && A.pair == E.pair;
+    stage = same && A.chunk > 0 && E.chunk > 0 ? 0 : E.chunk > 0 ? 2 : 3;
+    if (A.seq >= p.seq.nseq) stage = 6;
+    useq = A.seq;  // cursor of the whole units
+    upair = A.pair;
+    if (stage > 0 && A.chunk > 0 && ++upair == npairs) {
+      upair = 0;
+      ++useq;
+    }
+  }
+  __device__ __forceinline__ void next(const SsdPrefillParams& p, Run* out) {
+    Run run;
+    run.n = -1;
+    while (stage < 6) {
+      int pair, c1 = -1;
+      run.full = run.from_slot = true;
+      run.from_carry = run.awaited = run.publish = run.to_slot = false;
+      if (stage <= 1) {         // inside one unit: the range's own state, from zero; then in full
+        run.seq = A.seq; pair = A.pair; run.c0 = A.chunk; c1 = E.chunk;
+        run.from_slot = false;
+        run.full = run.from_carry = run.awaited = stage == 1;
+        run.publish = stage == 0;
+        stage = stage == 0 ? 1 : 6;
+      } else if (stage == 2) {  // the first part of the unit at the range's end
+        run.seq = E.seq; pair = E.pair; run.c0 = 0; c1 = E.chunk;
+        run.publish = true;
+        stage = same ? 6 : 3;
+      } else if (stage == 3) {  // whole units
+        if (useq == E.seq && upair == E.pair) {
+          stage = A.chunk > 0 ? 4 : 6;
+          continue;
+        }
+        run.seq = useq; pair = upair; run.c0 = 0;
+        run.to_slot = true;
+        if (++upair == npairs) { upair = 0; ++useq; }
+      } else {                  // the last part of the unit at the range's start
+        run.seq = A.seq; pair = A.pair; run.c0 = A.chunk;
+        run.from_slot = false;
+        run.from_carry = run.to_slot = true;
+        stage = 6;
+      }
+      run.slot = -1;
+      if (p.state) {
+        run.slot = claim_slot_warp(p.slots, run.seq, &g_fault_prefill);
+        if (run.slot < 0) {
+          if (stage == 1) stage = 6;  // the middle of a skipped sequence
+          continue;
+        }
+      }
+      run.begin = seq_begin(p.seq, run.seq);
+      run.end = seq_end(p.seq, run.seq, run.begin);
+      if (c1 < 0) c1 = (run.end - run.begin + kQ - 1) / kQ;
+      run.n = c1 - run.c0;  // 0 for an empty sequence: the state passes through
+      run.g = pair / ppg;
+      run.h0 = run.g * per + 2 * (pair - run.g * ppg);
+      run.nh2 = min(2, run.g * per + per - run.h0);  // an odd group's last pair holds one head
+      break;
+    }
+    if ((threadIdx.x & 31) == 0) *out = run;
+  }
+};
+
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const SsdPrefillParams p, int npairs, int blocks, const __grid_constant__ CUtensorMap map_x,
@@ -279,8 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sb = raw + pad;
   Arrays* const arr = reinterpret_cast<Arrays*>(sm + L::kArr);
   unsigned* const sMax = reinterpret_cast<unsigned*>(sm + L::kMax);
+  float* const sUn = reinterpret_cast<float*>(sm + L::kUn);
   uint32_t* const sslot = reinterpret_cast<uint32_t*>(sm + L::kSlot);
   __shared__ unsigned s_block;
+  __shared__ Run s_run[2];
   __shared__ int s_abort;
   auto bar = [&](int i) { return sb + L::kBars + 8u * static_cast<uint32_t>(i); };
 
@@ -292,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
 #pragma unroll
-    for (int i = 0; i < kNumBars; ++i) tc::mbar_init(bar(i), i < kNumTx ? 1 : i < kBarW ? 2 : i == kBarM || i >= kBarY ? 8 : 4);
+    for (int i = 0; i < kNumBars; ++i) tc::mbar_init(bar(i), i < kNumTx ? 1 : i == kBarM || i >= kBarY ? 8 : 4);
     tc::fence_mbar_init();
     s_abort = 0;
   }
@@ -316,13 +404,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   char* const ws = static_cast<char*>(p.ws);
   const PlanLayout play = plan_layout(p.seq.nseq, blocks, N);
-  const Cut* const cuts = reinterpret_cast<const Cut*>(ws + play.cuts);
   unsigned* const flags = reinterpret_cast<unsigned*>(ws + play.flags);
   float4* const carry = reinterpret_cast<float4*>(ws + play.carry);
-  if (tid == 0) s_block = atomicAdd(flags + blocks, 1u);
+  Runs runs;  // (the planning warp's)
+  if (warp == kPlanWarp) {
+    unsigned b = 0;
+    if (lane == 0) b = atomicAdd(flags + blocks, 1u);
+    b = __shfl_sync(0xffffffffu, b, 0);
+    if (lane == 0) s_block = b;
+    runs.start(p, reinterpret_cast<const Cut*>(ws + play.cuts) + b, npairs);
+    runs.next(p, s_run);
+  }
   __syncthreads();
   const int me = (int)s_block;
-  const Cut A = cuts[me], E = cuts[me + 1];
 
   // A wait that runs out, or that another thread's has, makes `ok` false; the
   // thread goes on to the next place where its role leaves the loop.
@@ -352,90 +446,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) arrive(bar(i));
   };
-  const int per = p.nheads / p.ngroups, ppg = (per + 1) / 2;  // heads and pairs per group
-  const bool same = A.seq == E.seq && A.pair == E.pair;
-  const bool middle = same && A.chunk > 0 && E.chunk > 0;
-  int stage = middle ? 0 : E.chunk > 0 ? 2 : 3;
-  if (A.seq >= p.seq.nseq) stage = 6;
-  int useq = A.seq, upair = A.pair;  // cursor of the whole units
-  if (!middle && A.chunk > 0) {
-    if (++upair == npairs) { upair = 0; ++useq; }
-  }
   uint32_t it = 0, itf = 0;  // chunks, and chunks in full, so far
 
-  // The next run: a unit, its chunks [c0, c0 + n), where its state comes from
-  // and goes to.  All threads of the block call it in step.
-  struct Run {
-    int seq, c0, n, begin, end, slot, g, h0, nh2;
-    bool full, from_slot, from_carry, publish, to_slot;
-    __device__ __forceinline__ int t0(int j) const { return begin + (c0 + j) * kQ; }
-  } run;
-  auto next = [&]() -> bool {
-    while (stage < 6) {
-      int pair, c1 = -1;
-      run.full = run.from_slot = true;
-      run.from_carry = run.publish = run.to_slot = false;
-      if (stage <= 1) {         // middle: the range's own state, from zero; then in full
-        run.seq = A.seq; pair = A.pair; run.c0 = A.chunk; c1 = E.chunk;
-        run.from_slot = false;
-        run.full = run.from_carry = stage == 1;
-        run.publish = stage == 0;
-        stage = stage == 0 ? 1 : 6;
-      } else if (stage == 2) {  // the first part of the unit at the range's end
-        run.seq = E.seq; pair = E.pair; run.c0 = 0; c1 = E.chunk;
-        run.publish = true;
-        stage = same ? 6 : 3;
-      } else if (stage == 3) {  // whole units
-        if (useq == E.seq && upair == E.pair) {
-          stage = A.chunk > 0 ? 4 : 6;
-          continue;
-        }
-        run.seq = useq; pair = upair; run.c0 = 0;
-        run.to_slot = true;
-        if (++upair == npairs) { upair = 0; ++useq; }
-      } else {                  // the last part of the unit at the range's start
-        run.seq = A.seq; pair = A.pair; run.c0 = A.chunk;
-        run.from_slot = false;
-        run.from_carry = run.to_slot = true;
-        stage = 6;
-      }
-      run.begin = seq_begin(p.seq, run.seq);
-      run.end = seq_end(p.seq, run.seq, run.begin);
-      if (c1 < 0) c1 = (run.end - run.begin + kQ - 1) / kQ;
-      run.n = c1 - run.c0;  // 0 for an empty sequence: the state passes through
-      run.slot = -1;
-      if (p.state) {
-        run.slot = claim_slot(p.slots, run.seq, &g_fault_prefill);
-        if (run.slot < 0) {
-          if (stage == 1) stage = 6;  // the middle of a skipped sequence
-          continue;
-        }
-      }
-      run.g = pair / ppg;
-      run.h0 = run.g * per + 2 * (pair - run.g * ppg);
-      run.nh2 = min(2, run.g * per + per - run.h0);  // an odd group's last pair holds one head
-      return true;
-    }
-    return false;
+  // Run r of the block: found by the planning warp while the run before is
+  // under way; false behind the last.
+  const Run* run = nullptr;
+  auto next = [&](uint32_t r) -> bool {
+    run = &s_run[r & 1];
+    return run->n >= 0;
   };
   // The run is done in all warps; false when the block gives up.
   auto done = [&]() -> bool {
-    it += run.n;
-    if (run.full) itf += run.n;
+    const int n = run->n;
+    it += n;
+    if (run->full) itf += n;
     return !__syncthreads_or(!ok);
   };
 
   if (warp < 8) {
-    while (next()) {
-      const int n = run.n, end = run.end, h0 = run.h0, nh2 = run.nh2;
-      const bool full = run.full;
+    for (uint32_t r = 0; next(r); ++r) {
+      const int n = run->n, end = run->end, h0 = run->h0, nh2 = run->nh2;
+      const bool full = run->full;
       // ----------------------------------------------------------- M and y
       const int h = h0 + min(hd, nh2 - 1);
       const bool mine = hd < nh2;
       const float Dh = p.D ? p.D[h] : 0.f;
       for (int j = 0; full && j < n; ++j) {
         const uint32_t k = it + j, kf = itf + j;
-        const int t0 = run.t0(j), nval = min(kQ, end - t0);
+        const int t0 = run->t0(j), nval = min(kQ, end - t0);
         const Arrays& a = arr[k & 1];
         unsigned char* const xs = sm + L::kX + (k & 1) * 32768 + hd * 16384;
         wait2(kBarA, k, 2);
@@ -538,12 +576,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsS));
-    while (next()) {
-      const int n = run.n, end = run.end, h0 = run.h0, nh2 = run.nh2;
-      const bool full = run.full;
-      // ----------------------------------------------------- Xw and the state
+    for (uint32_t r = 0; next(r); ++r) {
+      const int n = run->n, h0 = run->h0, nh2 = run->nh2;
+      const bool full = run->full;
+      // ----------------------------------------------------- the state -------
       const bool owns = hrow < nh2;
-      const int stid = tid - kGroupY, xh = blk >> 1, xc = 4 * (blk & 1);  // Xw: 32 columns of head xh, lanes over tokens
+      const int stid = tid - kGroupY;
       auto wait_flag = [&]() {  // the state that the block before publishes
         if (stid == 0) {
           uint32_t polls = 0, v = 0;
@@ -560,17 +598,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float4* const src = carry + (size_t)(me - 1) * (2 * kP * N / 4);
       // ---- the state entering the run
       float hs[N];
-      float* st = p.state && owns ? p.state + (((size_t)run.slot * p.nheads + h0) * kP + row) * N : nullptr;
+      float* st = p.state && owns ? p.state + (((size_t)run->slot * p.nheads + h0) * kP + row) * N : nullptr;
 #pragma unroll
       for (int i = 0; i < N; ++i) hs[i] = 0.f;
-      if (run.from_carry) {
-        if (!middle) wait_flag();  // the middle's first pass has waited already
+      if (run->from_carry) {
+        if (!run->awaited) wait_flag();
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
           const float4 v = __ldcg(src + i * kGroupS + stid);
           hs[4 * i] = v.x; hs[4 * i + 1] = v.y; hs[4 * i + 2] = v.z; hs[4 * i + 3] = v.w;
         }
-      } else if (run.from_slot && st && !(p.slots.fresh && p.slots.fresh[run.seq])) {
+      } else if (run->from_slot && st && !(p.slots.fresh && p.slots.fresh[run->seq])) {
 #pragma unroll
         for (int i = 0; i < N; i += 8) ld_v8(st + i, hs + i);
       }
@@ -587,13 +625,130 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = stid; i < 2048; i += kGroupS)
             *reinterpret_cast<uint4*>(sm + L::kX + (i >> 10) * 32768 + 16384 + 16 * (i & 1023)) = make_uint4(0, 0, 0, 0);
         signal(kBarH + (it & 1));
-        if (nh2 == 1) sync_s(false);
       }
       float psum = 0.f;  // log2 decay of the run so far (head hrow)
 
       for (int j = 0; j < n; ++j) {
         const uint32_t k = it + j, kf = itf + j;
-        const int nval = min(kQ, end - run.t0(j));
+        const Arrays& a = arr[k & 1];
+        wait2(kBarA, k, 2);
+        // ---- H <- 2^cs_last H + S
+        const float tot = (a.tot[hrow][0] + a.tot[hrow][1]) + (a.tot[hrow][2] + a.tot[hrow][3]);
+        psum += tot;
+        const float dec = ex2(tot);
+        if (full) wait(kBarYc, kf, 2);  // C H^T is done with the state copy
+        wait2(kBarSall, k, 2);
+        wait2(kBarR, k, 2);
+        tc::fence_after();
+        const f2_t dec2 = pk2(dec, dec), un2 = kBf16 ? 0 : pk2(sUn[2 * (k & 1) + hrow], sUn[2 * (k & 1) + hrow]);
+        const bool more = j + 1 < n;
+#pragma unroll
+        for (int q = 0; q < N; q += 16) {  // with the next chunk's 16-bit copy
+          float sv[16];
+          tc::ld32x32b_x16(tmem + lane_base + kS + q, sv);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            f2_t v = pk2(sv[i], sv[i + 1]);
+            if (!kBf16) v = mul2(v, un2);
+            v = fma2(dec2, pk2(hs[q + i], hs[q + i + 1]), v);
+            hs[q + i] = lo2(v);
+            hs[q + i + 1] = hi2(v);
+          }
+          if (more && full)
+#pragma unroll
+            for (int i = q / 8; i < q / 8 + 2; ++i)
+              *reinterpret_cast<uint4*>(sm + L::kH + (i / 8) * 16384 + swz(row, i % 8)) = pack8<T>(hs + 8 * i);
+        }
+        if (more) signal(kBarH + ((k + 1) & 1));
+      }
+      ok = !sync_s(!ok);
+
+      // ---- the state leaving the run
+      if (!full && ok && wait_flag()) {  // the middle of a unit: add what enters it, decayed
+        const float dec = ex2(psum);
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+          const float4 v = __ldcg(src + i * kGroupS + stid);
+          hs[4 * i] = fmaf(dec, v.x, hs[4 * i]);
+          hs[4 * i + 1] = fmaf(dec, v.y, hs[4 * i + 1]);
+          hs[4 * i + 2] = fmaf(dec, v.z, hs[4 * i + 2]);
+          hs[4 * i + 3] = fmaf(dec, v.w, hs[4 * i + 3]);
+        }
+      }
+      if (run->publish) {
+        float4* dst = carry + (size_t)me * (2 * kP * N / 4);
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+          dst[i * kGroupS + stid] = make_float4(hs[4 * i], hs[4 * i + 1], hs[4 * i + 2], hs[4 * i + 3]);
+        __threadfence();
+        sync_s(false);
+        if (stid == 0) asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(flags + me) : "memory");
+      } else if (run->to_slot && st) {
+#pragma unroll
+        for (int i = 0; i < N; i += 8) st_v8(st + i, hs + i);
+      }
+      if (!done()) break;
+    }
+  } else if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsX));
+    // ------------------------------------------------------ the decays and Xw
+    const int stid = tid - kGroupY - kGroupS, xh = blk >> 1, xc = 4 * (blk & 1);  // 32 columns of head xh, lanes over tokens
+    for (uint32_t r = 0; next(r); ++r) {
+      const int n = run->n, end = run->end, nh2 = run->nh2;
+      // Delta and the decays of the tokens of block blk, both heads
+      float dtn[2], A2[2], bias[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int h = run->h0 + min(e, nh2 - 1);
+        A2[e] = p.A[h] * kLog2e;
+        bias[e] = p.dt_bias ? p.dt_bias[h] : 0.f;
+      }
+      auto fetch = [&](int j) {
+        const int t = run->t0(j) + row;
+        const T* dtg = static_cast<const T*>(p.dt) + (int64_t)t * p.lddt + run->h0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) dtn[e] = j < n && t < end && e < nh2 ? Elt<T>::to_f(dtg[e]) : 0.f;
+      };
+      auto decays = [&](int j) {
+        Arrays& a = arr[(it + j) & 1];
+        float d[2], pre[2], suf[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float v = dtn[e] + bias[e];
+          d[e] = p.softplus ? softplus_f(v) : v;
+          if (run->t0(j) + row >= end || e >= nh2) d[e] = 0.f;
+          pre[e] = suf[e] = d[e] * A2[e];
+        }
+        fetch(j + 1);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float u = __shfl_up_sync(0xffffffffu, pre[e], o), v = __shfl_down_sync(0xffffffffu, suf[e], o);
+            if (lane >= o) pre[e] += u;
+            if (lane + o < 32) suf[e] += v;
+          }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float after = __shfl_down_sync(0xffffffffu, suf[e], 1);  // the tokens after this one
+          if (lane == 31) {
+            a.tot[e][blk] = pre[e];
+            after = 0.f;
+          }
+          a.f[e][row] = ex2(after) * d[e];
+          a.pre[e][row] = pre[e];
+          a.dl[e][row] = d[e];
+        }
+        __syncwarp();
+        if (lane == 0) arrive(bar(kBarA + ((it + j) & 1)));
+      };
+      if (n > 0) {
+        fetch(0);
+        decays(0);
+      }
+      for (int j = 0; j < n; ++j) {
+        const uint32_t k = it + j;
+        const int nval = min(kQ, end - run->t0(j));
         const Arrays& a = arr[k & 1];
         unsigned char* const xs = sm + L::kX + (k & 1) * 32768;
         wait2(kBarX, k, 1);
@@ -608,13 +763,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(xs + o) = zero;
             *reinterpret_cast<uint4*>(xs + 16384 + o) = zero;
           }
-          sync_s(false);
+          sync_x();
         }
         wait2(kBarA, k, 2);
-        float scale = 1.f, unscale = 1.f;
+        if (j == 0 && nh2 == 1) wait2(kBarH, k, 2);  // the missing head's x is cleared
+        float scale = 1.f;
         if constexpr (!kBf16) {  // fp16: the power of two that puts max (|x| Delta) below 2^15
           if (stid < 2) sMax[stid] = 0u;
-          sync_s(false);
+          sync_x();
 #pragma unroll 1
           for (int e = 0; e < 2; ++e) {
           unsigned m = 0;
@@ -630,13 +786,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           if (lane == 0) atomicMax(sMax + e, __float_as_uint(top));
           }
-          sync_s(false);
+          sync_x();
           auto power = [](unsigned v) {  // 2^(14 - exponent of v), within fp32's range
             const int e = (int)(v >> 23) - 127;
             return v == 0 ? 0 : min(100, max(-100, 14 - e));
           };
           scale = __uint_as_float((unsigned)(127 + power(sMax[xh])) << 23);
-          unscale = __uint_as_float((unsigned)(127 - power(sMax[hrow])) << 23);
+          if (stid < 2) sUn[2 * (k & 1) + stid] = __uint_as_float((unsigned)(127 - power(sMax[stid])) << 23);
         }
         // ---- Xw, 32 tokens at a time, as three 16-bit pieces
 #pragma unroll 1
@@ -647,8 +803,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const f2_t w2 = pk2(w, w), minus = pk2(-1.f, -1.f);
           const unsigned char* const from = xs + xh * 16384;
           unsigned char* const to = sm + L::kW + (q & 1) * 24576 + xh * 4096;
-          if (q > 1) wait(kBarS + (q & 1), 0, 2);  // the products of the quarter before the last have read the buffer
-#pragma unroll 1
+          // the products of the quarter before the last have read the buffer
+          if (q > 1 || j > 0) wait(kBarS + (q & 1), q > 1 ? 0 : 1, 2);
+#pragma unroll 2
           for (int k4 = xc; k4 < xc + 4; ++k4) {
             const uint4 xv = *reinterpret_cast<const uint4*>(from + swz(32 * q + lane, k4));
             const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
@@ -671,83 +828,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(to + 16384 + o) = make_uint4(z[0], z[1], z[2], z[3]);
           }
           signal(kBarW + (q & 1));
+          if (q == 1 && j + 1 < n) {  // the next chunk's decays, when the readers of the chunk before are done with the buffer
+            if (j > 0) wait2(kBarH, k, 2);
+            if (j > 0 && run->full) wait2(kBarY, itf + j - 1, 2);
+            decays(j + 1);
+          }
         }
         if (lane == 0) arrive(bar(kBarR + (k & 1)));  // (the signal above ordered the warp's accesses)
-        // ---- H <- 2^cs_last H + S
-        const float tot = (a.tot[hrow][0] + a.tot[hrow][1]) + (a.tot[hrow][2] + a.tot[hrow][3]);
-        psum += tot;
-        const float dec = ex2(tot);
-        if (full) wait(kBarYc, kf, 2);  // C H^T is done with the state copy
-        wait(kBarS + 1, 1, 2);
-        tc::fence_after();
-        const f2_t dec2 = pk2(dec, dec), un2 = pk2(unscale, unscale);
-        const bool more = j + 1 < n;
-#pragma unroll
-        for (int q = 0; q < N; q += 32) {  // with the next chunk's 16-bit copy
-          float sv[32];
-          tc::ld32x32b_x32(tmem + lane_base + kS + q, sv);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            f2_t v = pk2(sv[i], sv[i + 1]);
-            if (!kBf16) v = mul2(v, un2);
-            v = fma2(dec2, pk2(hs[q + i], hs[q + i + 1]), v);
-            hs[q + i] = lo2(v);
-            hs[q + i + 1] = hi2(v);
-          }
-          if (more && full)
-#pragma unroll
-            for (int i = q / 8; i < q / 8 + 4; ++i)
-              *reinterpret_cast<uint4*>(sm + L::kH + (i / 8) * 16384 + swz(row, i % 8)) = pack8<T>(hs + 8 * i);
-        }
-        if (more) signal(kBarH + ((k + 1) & 1));
-      }
-      ok = !sync_s(!ok);
-
-      // ---- the state leaving the run
-      if (!full && ok && wait_flag()) {  // the middle of a unit: add what enters it, decayed
-        const float dec = ex2(psum);
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-          const float4 v = __ldcg(src + i * kGroupS + stid);
-          hs[4 * i] = fmaf(dec, v.x, hs[4 * i]);
-          hs[4 * i + 1] = fmaf(dec, v.y, hs[4 * i + 1]);
-          hs[4 * i + 2] = fmaf(dec, v.z, hs[4 * i + 2]);
-          hs[4 * i + 3] = fmaf(dec, v.w, hs[4 * i + 3]);
-        }
-      }
-      if (run.publish) {
-        float4* dst = carry + (size_t)me * (2 * kP * N / 4);
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i)
-          dst[i * kGroupS + stid] = make_float4(hs[4 * i], hs[4 * i + 1], hs[4 * i + 2], hs[4 * i + 3]);
-        __threadfence();
-        sync_s(false);
-        if (stid == 0) asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(flags + me) : "memory");
-      } else if (run.to_slot && st) {
-#pragma unroll
-        for (int i = 0; i < N; i += 8) st_v8(st + i, hs + i);
       }
       if (!done()) break;
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsHelp));
   if (warp == kTmaWarp) {
-    while (next()) {
-      const int n = run.n, c0 = run.c0, c1 = c0 + n, end = run.end, h0 = run.h0, nh2 = run.nh2;
-      const bool full = run.full;
+    for (uint32_t r = 0; next(r); ++r) {
+      const int n = run->n, c0 = run->c0, c1 = c0 + n, end = run->end, h0 = run->h0, nh2 = run->nh2;
+      const bool full = run->full;
       // ------------------------------------------------------------ copies
       if (lane == 0 && n > 0) {
         auto load = [&](int i, uint32_t off, const CUtensorMap* map, int col, int c, int nb) {
           tc::expect_tx(bar(i), 16384u * nb);
-          for (int b = 0; b < nb; ++b) tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, run.begin + c * kQ, bar(i));
+          for (int b = 0; b < nb; ++b) tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, run->begin + c * kQ, bar(i));
           arm(i);
         };
-        auto load_b = [&](int c) { load(kBarB, L::kB, &map_b, run.g * N, c, N / 64); };
-        auto load_c = [&](int c) { load(kBarC, L::kC, &map_c, run.g * N, c, N / 64); };
+        auto load_b = [&](int c) { load(kBarB, L::kB, &map_b, run->g * N, c, N / 64); };
+        auto load_c = [&](int c) { load(kBarC, L::kC, &map_c, run->g * N, c, N / 64); };
         auto load_x = [&](int c, uint32_t k) { load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, c, nh2); };
         auto store_y = [&](int c, uint32_t k) {
           for (int b = 0; b < nh2; ++b)
-            tc::tma_store_2d(&map_y, (h0 + b) * kP, run.begin + c * kQ, sb + L::kX + (k & 1) * 32768 + 16384u * b);
+            tc::tma_store_2d(&map_y, (h0 + b) * kP, run->begin + c * kQ, sb + L::kX + (k & 1) * 32768 + 16384u * b);
           tc::bulk_commit();
         };
         load_x(c0, it);
@@ -774,160 +883,103 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (full && ok) {
           wait2(kBarY, itf + n - 1, 2);
-          if (ok && run.t0(n) <= end) store_y(c1 - 1, it + n - 1);  // a ragged chunk is written by the y group
+          if (ok && run->t0(n) <= end) store_y(c1 - 1, it + n - 1);  // a ragged chunk is written by the y group
         }
         tc::bulk_wait_read_all();
       }
       __syncwarp();
       if (!done()) break;
     }
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ products
-    // One warp issues them all.  It follows two sequences, the products of y and
-    // those of the state, and issues the next batch of whichever is ready.  The
-    // issuing lane is picked by elect.sync: in a branch on the thread number
-    // the compiler cannot take descriptors for uniform, and a product of
-    // 128 x 128 x 16 takes 170-220 cycles to issue instead of 66 to execute.
-    while (next()) {
-      const int n = run.n, end = run.end;
-      {
-        auto ready = [&](int i, uint32_t parity) { return tc::test(bar(i), parity & 1u); };
-        auto ready2 = [&](int i, uint32_t k) { return ready(i + (int)(k & 1), k >> 1); };
-        int jy = run.full ? 0 : n, js = 0, sy = 0, q = 0;  // chunk and step of either sequence
-        uint32_t idle = 0;
-        while (ok && (jy < n || js < n)) {
-          bool issued = false;
-          if (js < n) {
-            const uint32_t k = it + js;
-            if (ready(kBarW + (q & 1), q >> 1) && ready(kBarB, k) && ready2(kBarH, k)) {
-              tc::fence_after();
-              if (tc::elect()) {
-                const uint64_t dbm = tc::desc_sw128(sb + L::kB + q * 4096, 16384, 1024);
-                const uint64_t dw = tc::desc_sw128(sb + L::kW + (q & 1) * 24576, 4096, 1024);
-#pragma unroll 1
-                for (int i = 0; i < 6; ++i)  // three pieces, two steps of 16 tokens
-                  tc::mma(tmem + kS, dw + ((i >> 1) * 8192 + (i & 1) * 2048) / 16, dbm + (i & 1) * (2048 >> 4), kIdS,
-                          (q | i) != 0);
-                tc::commit(bar(kBarS + (q & 1)));
-                if (q == 3) tc::commit(bar(kBarSall + (k & 1)));
-              }
-              __syncwarp();
-              arm(kBarS + (q & 1));
-              if (q == 3) {
-                arm(kBarSall + (k & 1));
-                ++js;
-              }
-              q = (q + 1) & 3;
-              issued = true;
-            }
+  } else if (warp == kMmaY) {
+    // Products.  The issuing lane is picked by elect.sync: in a branch on the
+    // thread number the compiler cannot take descriptors for uniform, and a
+    // product of 128 x 128 x 16 takes 170-220 cycles to issue instead of the
+    // 66 it takes to execute.
+    // ----------------------------------------------------- products of y
+    const uint64_t dc = tc::desc_sw128(sb + L::kC, 16, 1024), db = tc::desc_sw128(sb + L::kB, 16, 1024),
+                   dh = tc::desc_sw128(sb + L::kH, 16, 1024), dx0 = tc::desc_sw128(sb + L::kX, 16384, 1024);
+    for (uint32_t r = 0; next(r); ++r) {
+      const int n = run->full ? run->n : 0;
+      for (int j = 0; j < n && ok; ++j) {
+        const uint32_t k = it + j, kf = itf + j;
+        wait(kBarB, k, 1);
+        wait(kBarC, kf, 1);
+        if (j > 0) wait2(kBarY, kf - 1, 2);  // the accumulators are read
+        if (!ok) break;
+        tc::fence_after();
+        if (tc::elect()) {
+#pragma unroll
+          for (int kk = 0; kk < N / 16; ++kk) {
+            const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+            tc::mma(tmem + kG, dc + ko, db + ko, kId, kk > 0);
           }
-          if (jy < n) {
-            const uint32_t k = it + jy, kf = itf + jy;
-            if (sy < 2) {
-              const bool go = sy == 0 ? ready(kBarB, k) && ready(kBarC, kf) && (jy == 0 || ready2(kBarY, kf - 1))
-                                      : ready2(kBarH, k);
-              if (go) {  // G = C B^T; Yc = C H^T
-                tc::fence_after();
-                const int b = sy == 0 ? kBarG : kBarYc;
-                if (tc::elect()) {
-                  const uint64_t dc = tc::desc_sw128(sb + L::kC, 16, 1024);
-                  const uint64_t db = tc::desc_sw128(sb + (sy == 0 ? L::kB : L::kH), 16, 1024);
-                  const uint32_t to = tmem + (sy == 0 ? kG : kYc);
-#pragma unroll 1
-                  for (int kk = 0; kk < N / 16; ++kk) {
-                    const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-                    tc::mma(to, dc + ko, db + ko, kId, kk > 0);
-                  }
-                  tc::commit(bar(b));
-                }
-                __syncwarp();
-                arm(b);
-                ++sy;
-                issued = true;
-              }
-            } else if (ready(kBarM, kf) && ready2(kBarX, k) && (run.t0(jy + 1) <= end || ready2(kBarR, k))) {
-              tc::fence_after();  // (a ragged chunk's x is cleared behind its end before kBarR)
-              if (tc::elect()) {
-                const uint64_t dx = tc::desc_sw128(sb + L::kX + (k & 1) * 32768, 16384, 1024);
-#pragma unroll 1
-                for (int i = 0; i < 16; ++i)  // two heads, 8 steps of 16 tokens; the second head's x is 16 KB on
-                  tc::mma_ta(tmem + kG + 64 * (i >> 3), tmem + kM + 8 * i, dx + i * (2048 >> 4), kIdYm, (i & 7) != 0);
-                tc::commit(bar(kBarYm));
-              }
-              __syncwarp();
-              arm(kBarYm);
-              sy = 0;
-              ++jy;
-              issued = true;
-            }
-          }
-          if (issued) {
-            idle = 0;
-          } else {
-            if (++idle == kWaitLimit * 8) s_abort = 2;
-            if (*reinterpret_cast<volatile int*>(&s_abort)) ok = false;
-          }
+          tc::commit(bar(kBarG));
         }
+        __syncwarp();
+        arm(kBarG);
+        wait2(kBarH, k, 2);
+        if (!ok) break;
+        tc::fence_after();
+        if (tc::elect()) {
+#pragma unroll
+          for (int kk = 0; kk < N / 16; ++kk) {
+            const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+            tc::mma(tmem + kYc, dc + ko, dh + ko, kId, kk > 0);
+          }
+          tc::commit(bar(kBarYc));
+        }
+        __syncwarp();
+        arm(kBarYc);
+        wait2(kBarX, k, 1);
+        wait(kBarM, kf, 2);
+        if (run->t0(j + 1) > run->end) wait2(kBarR, k, 2);  // a ragged chunk's x is cleared behind its end
+        if (!ok) break;
+        tc::fence_after();
+        if (tc::elect()) {
+          const uint64_t dx = dx0 + (k & 1) * (32768 >> 4);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)  // two heads, 8 steps of 16 tokens; the second head's x is 16 KB on
+            tc::mma_ta(tmem + kG + 64 * (i >> 3), tmem + kM + 8 * i, dx + i * (2048 >> 4), kIdYm, (i & 7) != 0);
+          tc::commit(bar(kBarYm));
+        }
+        __syncwarp();
+        arm(kBarYm);
       }
-      __syncwarp();
+      if (!done()) break;
+    }
+  } else if (warp == kMmaS) {
+    // --------------------------------------------- products of the state
+    const uint64_t db = tc::desc_sw128(sb + L::kB, 16384, 1024), dw0 = tc::desc_sw128(sb + L::kW, 4096, 1024);
+    for (uint32_t r = 0; next(r); ++r) {
+      const int n = run->n;
+      for (int j = 0; j < n && ok; ++j) {
+        const uint32_t k = it + j;
+        wait(kBarB, k, 1);
+        wait2(kBarH, k, 2);
+        for (int q = 0; q < 4; ++q) {
+          wait(kBarW + (q & 1), q >> 1, 2);
+          if (!ok) break;
+          tc::fence_after();
+          if (tc::elect()) {
+            const uint64_t dw = dw0 + (q & 1) * (24576 >> 4), dbq = db + q * (4096 >> 4);
+#pragma unroll
+            for (int i = 0; i < 6; ++i)  // three pieces, two steps of 16 tokens
+              tc::mma(tmem + kS, dw + ((i >> 1) * 8192 + (i & 1) * 2048) / 16, dbq + (i & 1) * (2048 >> 4), kIdS,
+                      (q | i) != 0);
+            tc::commit(bar(kBarS + (q & 1)));
+            if (q == 3) tc::commit(bar(kBarSall + (k & 1)));
+          }
+          __syncwarp();
+          arm(kBarS + (q & 1));
+        }
+        if (!ok) break;
+        arm(kBarSall + (k & 1));
+      }
       if (!done()) break;
     }
   } else {
-    // ------------------------- Delta and the decays of a head, a chunk ahead
-    const int e = warp - kDecayWarp;
-    while (next()) {
-      const int n = run.n, end = run.end, h = run.h0 + min(e, run.nh2 - 1);
-      const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-      const T* const dtg = static_cast<const T*>(p.dt) + h;
-      const bool have = e < run.nh2;
-      float dtn[4];  // token 32 b + lane
-      auto fetch = [&](int j) {
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int t = run.t0(j) + 32 * b + lane;
-          dtn[b] = j < n && t < end ? Elt<T>::to_f(dtg[(int64_t)t * p.lddt]) : 0.f;
-        }
-      };
-      fetch(0);
-#pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        const uint32_t k = it + j;
-        float d[4], pre[4], suf[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const float v = dtn[b] + bias;
-          d[b] = p.softplus ? softplus_f(v) : v;
-          if (run.t0(j) + 32 * b + lane >= end || !have) d[b] = 0.f;
-          pre[b] = suf[b] = d[b] * A2;
-        }
-        fetch(j + 1);
-#pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const float u = __shfl_up_sync(0xffffffffu, pre[b], o), v = __shfl_down_sync(0xffffffffu, suf[b], o);
-            if (lane >= o) pre[b] += u;
-            if (lane + o < 32) suf[b] += v;
-          }
-        // the readers of this buffer, two chunks before
-        if (j > 1) wait2(kBarH, k - 1, 2);
-        if (j > 1 && run.full) wait2(kBarY, itf + j - 2, 2);
-        Arrays& a = arr[k & 1];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int r = 32 * b + lane;
-          float after = __shfl_down_sync(0xffffffffu, suf[b], 1);  // the tokens after this one
-          if (lane == 31) {
-            a.tot[e][b] = pre[b];
-            after = 0.f;
-          }
-          a.f[e][r] = ex2(after) * d[b];
-          a.pre[e][r] = pre[b];
-          a.dl[e][r] = d[b];
-        }
-        __syncwarp();
-        if (lane == 0) arrive(bar(kBarA + (k & 1)));
-      }
+    for (uint32_t r = 0; next(r); ++r) {
+      runs.next(p, &s_run[(r + 1) & 1]);
       if (!done()) break;
     }
   }
@@ -935,11 +987,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Drain: copies and products in flight must be done before shared memory and
   // TMEM are given back (a no-op on the normal path, but for the last y).
-  if (lane == 0 && warp >= 12) {
-#pragma unroll
-    for (int i = 0; i < kNumTx; ++i)
-      if ((armed >> i) & 1u)
-        if (!tc::wait(bar(i), (last_par >> i) & 1u, kWaitLimit)) atomicOr(&g_fault_prefill, 4u);
+  if (lane == 0 && warp >= 16) {
+    bool drained = true;
+#pragma unroll 1
+    for (int i = 0; i < kNumTx; ++i) {
+      if (!((armed >> i) & 1u)) continue;
+      uint32_t polls = 0;
+#pragma unroll 1
+      while (!tc::wait(bar(i), (last_par >> i) & 1u, 1) && ++polls < kWaitLimit) {}
+      drained &= polls < kWaitLimit;
+    }
+    if (!drained) atomicOr(&g_fault_prefill, 4u);
     tc::bulk_wait_all();
   }
   tc::fence_before();
