@@ -471,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int h = h0 + min(hd, nh2 - 1);
       const bool mine = hd < nh2;
       const float Dh = p.D ? p.D[h] : 0.f;
+#pragma unroll 1
       for (int j = 0; full && j < n; ++j) {
         const uint32_t k = it + j, kf = itf + j;
         const int t0 = run->t0(j), nval = min(kQ, end - t0);
@@ -628,6 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float psum = 0.f;  // log2 decay of the run so far (head hrow)
 
+#pragma unroll 1
       for (int j = 0; j < n; ++j) {
         const uint32_t k = it + j, kf = itf + j;
         const Arrays& a = arr[k & 1];
@@ -746,6 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fetch(0);
         decays(0);
       }
+#pragma unroll 1
       for (int j = 0; j < n; ++j) {
         const uint32_t k = it + j;
         const int nval = min(kQ, end - run->t0(j));
@@ -848,6 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && n > 0) {
         auto load = [&](int i, uint32_t off, const CUtensorMap* map, int col, int c, int nb) {
           tc::expect_tx(bar(i), 16384u * nb);
+#pragma unroll 1
           for (int b = 0; b < nb; ++b) tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, run->begin + c * kQ, bar(i));
           arm(i);
         };
@@ -855,6 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto load_c = [&](int c) { load(kBarC, L::kC, &map_c, run->g * N, c, N / 64); };
         auto load_x = [&](int c, uint32_t k) { load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, c, nh2); };
         auto store_y = [&](int c, uint32_t k) {
+#pragma unroll 1
           for (int b = 0; b < nh2; ++b)
             tc::tma_store_2d(&map_y, (h0 + b) * kP, run->begin + c * kQ, sb + L::kX + (k & 1) * 32768 + 16384u * b);
           tc::bulk_commit();
@@ -862,6 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         load_x(c0, it);
         load_b(c0);
         if (full) load_c(c0);
+#pragma unroll 1
         for (int j = 0; j < n && ok; ++j) {  // each buffer is loaded again as its last reader is done
           const int c = c0 + j;
           const uint32_t k = it + j, kf = itf + j;
@@ -900,6 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    dh = tc::desc_sw128(sb + L::kH, 16, 1024), dx0 = tc::desc_sw128(sb + L::kX, 16384, 1024);
     for (uint32_t r = 0; next(r); ++r) {
       const int n = run->full ? run->n : 0;
+#pragma unroll 1
       for (int j = 0; j < n && ok; ++j) {
         const uint32_t k = it + j, kf = itf + j;
         wait(kBarB, k, 1);
@@ -908,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc::fence_after();
         if (tc::elect()) {
-#pragma unroll
+#pragma unroll 1
           for (int kk = 0; kk < N / 16; ++kk) {
             const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
             tc::mma(tmem + kG, dc + ko, db + ko, kId, kk > 0);
@@ -921,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc::fence_after();
         if (tc::elect()) {
-#pragma unroll
+#pragma unroll 1
           for (int kk = 0; kk < N / 16; ++kk) {
             const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
             tc::mma(tmem + kYc, dc + ko, dh + ko, kId, kk > 0);
@@ -937,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_after();
         if (tc::elect()) {
           const uint64_t dx = dx0 + (k & 1) * (32768 >> 4);
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < 16; ++i)  // two heads, 8 steps of 16 tokens; the second head's x is 16 KB on
             tc::mma_ta(tmem + kG + 64 * (i >> 3), tmem + kM + 8 * i, dx + i * (2048 >> 4), kIdYm, (i & 7) != 0);
           tc::commit(bar(kBarYm));
@@ -952,17 +959,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t db = tc::desc_sw128(sb + L::kB, 16384, 1024), dw0 = tc::desc_sw128(sb + L::kW, 4096, 1024);
     for (uint32_t r = 0; next(r); ++r) {
       const int n = run->n;
+#pragma unroll 1
       for (int j = 0; j < n && ok; ++j) {
         const uint32_t k = it + j;
         wait(kBarB, k, 1);
         wait2(kBarH, k, 2);
+#pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           wait(kBarW + (q & 1), q >> 1, 2);
           if (!ok) break;
           tc::fence_after();
           if (tc::elect()) {
             const uint64_t dw = dw0 + (q & 1) * (24576 >> 4), dbq = db + q * (4096 >> 4);
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < 6; ++i)  // three pieces, two steps of 16 tokens
               tc::mma(tmem + kS, dw + ((i >> 1) * 8192 + (i & 1) * 2048) / 16, dbq + (i & 1) * (2048 >> 4), kIdS,
                       (q | i) != 0);
