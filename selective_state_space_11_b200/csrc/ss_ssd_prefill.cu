@@ -68,8 +68,8 @@ namespace {
 constexpr int kP = 64;         // head dimension
 constexpr int kQ = 128;        // chunk length
 // Warps: 0-7 form M and y (a warpgroup per head), 8-11 hold the state, 12-15
-// form the decays and Xw, then one for the products of y, one for those of the
-// state, one for the copies, and one that finds the block's next run.  The registers of a block, 96 per thread at launch, are split
+// form Xw, then one for the products of y, one for those of the state, one for
+// the copies, and one that forms the decays and finds the block's next run.  The registers of a block, 96 per thread at launch, are split
 // unevenly: the state's warps hold a whole state row each.
 constexpr int kGroupY = 256, kGroupS = 128;  // threads of the y group, of the state's and Xw's
 constexpr int kMmaY = 16, kMmaS = 17, kTmaWarp = 18, kPlanWarp = 19;
@@ -273,7 +273,7 @@ struct Run {
   __device__ __forceinline__ int t0(int j) const { return begin + (c0 + j) * kQ; }
 };
 
-// Finds the runs of a block one after the other (all lanes of a warp in step).
+// Finds the runs of a block one after the other (in shared memory; all lanes of a warp call next).
 struct Runs {
   Cut A, E;
   int stage, useq, upair, npairs, per, ppg;
@@ -298,6 +298,8 @@ struct Runs {
   __device__ __forceinline__ void next(const SsdPrefillParams& p, Run* out) {
     Run run;
     run.n = -1;
+    int stage = this->stage, useq = this->useq, upair = this->upair;
+    __syncwarp();
     while (stage < 6) {
       int pair, c1 = -1;
       run.full = run.from_slot = true;
@@ -343,7 +345,13 @@ struct Runs {
       run.nh2 = min(2, run.g * per + per - run.h0);  // an odd group's last pair holds one head
       break;
     }
-    if ((threadIdx.x & 31) == 0) *out = run;
+    if ((threadIdx.x & 31) == 0) {
+      *out = run;
+      this->stage = stage;
+      this->useq = useq;
+      this->upair = upair;
+    }
+    __syncwarp();
   }
 };
 
@@ -369,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* const sslot = reinterpret_cast<uint32_t*>(sm + L::kSlot);
   __shared__ unsigned s_block;
   __shared__ Run s_run[2];
-  __shared__ int s_abort;
+  __shared__ Runs s_runs;
   auto bar = [&](int i) { return sb + L::kBars + 8u * static_cast<uint32_t>(i); };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -380,9 +388,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
 #pragma unroll
-    for (int i = 0; i < kNumBars; ++i) tc::mbar_init(bar(i), i < kNumTx ? 1 : i == kBarM || i >= kBarY ? 8 : 4);
+    for (int i = 0; i < kNumBars; ++i) tc::mbar_init(bar(i), i < kBarW ? 1 : i == kBarM || i >= kBarY ? 8 : 4);
     tc::fence_mbar_init();
-    s_abort = 0;
   }
   if (tid == 32 * kTmaWarp) {
     tc::prefetch_map(&map_x);
@@ -406,30 +413,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PlanLayout play = plan_layout(p.seq.nseq, blocks, N);
   unsigned* const flags = reinterpret_cast<unsigned*>(ws + play.flags);
   float4* const carry = reinterpret_cast<float4*>(ws + play.carry);
-  Runs runs;  // (the planning warp's)
   if (warp == kPlanWarp) {
     unsigned b = 0;
     if (lane == 0) b = atomicAdd(flags + blocks, 1u);
     b = __shfl_sync(0xffffffffu, b, 0);
     if (lane == 0) s_block = b;
-    runs.start(p, reinterpret_cast<const Cut*>(ws + play.cuts) + b, npairs);
-    runs.next(p, s_run);
+    if (lane == 0) s_runs.start(p, reinterpret_cast<const Cut*>(ws + play.cuts) + b, npairs);
+    __syncwarp();
+    s_runs.next(p, s_run);
   }
   __syncthreads();
   const int me = (int)s_block;
 
-  // A wait that runs out, or that another thread's has, makes `ok` false; the
-  // thread goes on to the next place where its role leaves the loop.
+  // A wait that runs out makes the thread's `ok` false: it waits for nothing
+  // any more, and its role leaves its loop where all of the role's warps can.
   bool ok = true;
-  auto wait = [&](int i, uint32_t parity, int bit) {
-    uint32_t n = 0;
-    while (ok && !tc::wait(bar(i), parity & 1u, 1)) {
-      if (++n == kWaitLimit) s_abort = bit;
-      if (*reinterpret_cast<volatile int*>(&s_abort)) ok = false;
-    }
+  auto wait = [&](int i, uint32_t parity) {
+    if (ok) ok = tc::wait_until(bar(i), parity & 1u, kWaitLimit);
   };
   // the pairs that alternate between chunks
-  auto wait2 = [&](int i, uint32_t k, int bit) { wait(i + (int)(k & 1), k >> 1, bit); };
+  auto wait2 = [&](int i, uint32_t k) { wait(i + (int)(k & 1), k >> 1); };
   // barriers that the copy and the product thread have armed, and the parity
   // of the last phase, for the drain
   uint32_t armed = 0, last_par = 0, next_par = 0;
@@ -477,9 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t0 = run->t0(j), nval = min(kQ, end - t0);
         const Arrays& a = arr[k & 1];
         unsigned char* const xs = sm + L::kX + (k & 1) * 32768 + hd * 16384;
-        wait2(kBarA, k, 2);
+        wait2(kBarA, k);
         const float pre = a.pre[hd][row];
-        wait(kBarG, kf, 2);
+        wait(kBarG, kf);
         tc::fence_after();
         // ---- M, row `row`: 32 columns at a time, from the diagonal block to the left
         float between = pre;  // log2 decay from the end of block i to this row
@@ -527,10 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const f2_t e2 = pk2(e, e), D2 = pk2(Dh, Dh);
         const int64_t t = t0 + row;
         const T* zg = p.z && mine && row < nval ? static_cast<const T*>(p.z) + t * p.ldz + h * kP : nullptr;
-        wait2(kBarX, k, 1);
-        wait(kBarYc, kf, 2);
-        wait2(kBarR, k, 2);
-        wait(kBarYm, kf, 2);
+        wait2(kBarX, k);
+        wait(kBarYc, kf);
+        wait2(kBarR, k);
+        wait(kBarYm, kf);
         tc::fence_after();
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
@@ -589,10 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           do {
             asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flags + me - 1) : "memory");
           } while (!v && ++polls < kFlagLimit);
-          if (!v) {
-            s_abort = 2;
-            ok = false;
-          }
+          if (!v) ok = false;
         }
         return !sync_s(!ok);
       };
@@ -633,14 +633,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < n; ++j) {
         const uint32_t k = it + j, kf = itf + j;
         const Arrays& a = arr[k & 1];
-        wait2(kBarA, k, 2);
+        wait2(kBarA, k);
         // ---- H <- 2^cs_last H + S
         const float tot = (a.tot[hrow][0] + a.tot[hrow][1]) + (a.tot[hrow][2] + a.tot[hrow][3]);
         psum += tot;
         const float dec = ex2(tot);
-        if (full) wait(kBarYc, kf, 2);  // C H^T is done with the state copy
-        wait2(kBarSall, k, 2);
-        wait2(kBarR, k, 2);
+        if (full) wait(kBarYc, kf);  // C H^T is done with the state copy
+        wait2(kBarSall, k);
+        wait2(kBarR, k);
         tc::fence_after();
         const f2_t dec2 = pk2(dec, dec), un2 = kBf16 ? 0 : pk2(sUn[2 * (k & 1) + hrow], sUn[2 * (k & 1) + hrow]);
         const bool more = j + 1 < n;
@@ -693,70 +693,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsX));
-    // ------------------------------------------------------ the decays and Xw
+    // ----------------------------------------------------------------- Xw
     const int stid = tid - kGroupY - kGroupS, xh = blk >> 1, xc = 4 * (blk & 1);  // 32 columns of head xh, lanes over tokens
     for (uint32_t r = 0; next(r); ++r) {
       const int n = run->n, end = run->end, nh2 = run->nh2;
-      // Delta and the decays of the tokens of block blk, both heads
-      float dtn[2], A2[2], bias[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int h = run->h0 + min(e, nh2 - 1);
-        A2[e] = p.A[h] * kLog2e;
-        bias[e] = p.dt_bias ? p.dt_bias[h] : 0.f;
-      }
-      auto fetch = [&](int j) {
-        const int t = run->t0(j) + row;
-        const T* dtg = static_cast<const T*>(p.dt) + (int64_t)t * p.lddt + run->h0;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) dtn[e] = j < n && t < end && e < nh2 ? Elt<T>::to_f(dtg[e]) : 0.f;
-      };
-      auto decays = [&](int j) {
-        Arrays& a = arr[(it + j) & 1];
-        float d[2], pre[2], suf[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float v = dtn[e] + bias[e];
-          d[e] = p.softplus ? softplus_f(v) : v;
-          if (run->t0(j) + row >= end || e >= nh2) d[e] = 0.f;
-          pre[e] = suf[e] = d[e] * A2[e];
-        }
-        fetch(j + 1);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float u = __shfl_up_sync(0xffffffffu, pre[e], o), v = __shfl_down_sync(0xffffffffu, suf[e], o);
-            if (lane >= o) pre[e] += u;
-            if (lane + o < 32) suf[e] += v;
-          }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float after = __shfl_down_sync(0xffffffffu, suf[e], 1);  // the tokens after this one
-          if (lane == 31) {
-            a.tot[e][blk] = pre[e];
-            after = 0.f;
-          }
-          a.f[e][row] = ex2(after) * d[e];
-          a.pre[e][row] = pre[e];
-          a.dl[e][row] = d[e];
-        }
-        __syncwarp();
-        if (lane == 0) arrive(bar(kBarA + ((it + j) & 1)));
-      };
-      if (n > 0) {
-        fetch(0);
-        decays(0);
-      }
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
         const uint32_t k = it + j;
         const int nval = min(kQ, end - run->t0(j));
         const Arrays& a = arr[k & 1];
         unsigned char* const xs = sm + L::kX + (k & 1) * 32768;
-        wait2(kBarX, k, 1);
+        wait2(kBarX, k);
         if (nval < kQ) {  // rows behind the sequence belong to others: no NaN of theirs may meet a zero weight
-          wait(kBarB, k, 1);
+          wait(kBarB, k);
           const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
           for (int i = stid; i < (kQ - nval) * 8; i += kGroupS) {
@@ -768,8 +717,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           sync_x();
         }
-        wait2(kBarA, k, 2);
-        if (j == 0 && nh2 == 1) wait2(kBarH, k, 2);  // the missing head's x is cleared
+        wait2(kBarA, k);
+        if (j == 0 && nh2 == 1) wait2(kBarH, k);  // the missing head's x is cleared
         float scale = 1.f;
         if constexpr (!kBf16) {  // fp16: the power of two that puts max (|x| Delta) below 2^15
           if (stid < 2) sMax[stid] = 0u;
@@ -807,8 +756,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const unsigned char* const from = xs + xh * 16384;
           unsigned char* const to = sm + L::kW + (q & 1) * 24576 + xh * 4096;
           // the products of the quarter before the last have read the buffer
-          if (q > 1 || j > 0) wait(kBarS + (q & 1), q > 1 ? 0 : 1, 2);
-#pragma unroll 2
+          if (q > 1 || j > 0) wait(kBarS + (q & 1), q > 1 ? 0 : 1);
+#pragma unroll 1
           for (int k4 = xc; k4 < xc + 4; ++k4) {
             const uint4 xv = *reinterpret_cast<const uint4*>(from + swz(32 * q + lane, k4));
             const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
@@ -831,11 +780,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(to + 16384 + o) = make_uint4(z[0], z[1], z[2], z[3]);
           }
           signal(kBarW + (q & 1));
-          if (q == 1 && j + 1 < n) {  // the next chunk's decays, when the readers of the chunk before are done with the buffer
-            if (j > 0) wait2(kBarH, k, 2);
-            if (j > 0 && run->full) wait2(kBarY, itf + j - 1, 2);
-            decays(j + 1);
-          }
         }
         if (lane == 0) arrive(bar(kBarR + (k & 1)));  // (the signal above ordered the warp's accesses)
       }
@@ -845,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsHelp));
   if (warp == kTmaWarp) {
     for (uint32_t r = 0; next(r); ++r) {
-      const int n = run->n, c0 = run->c0, c1 = c0 + n, end = run->end, h0 = run->h0, nh2 = run->nh2;
+      const int n = run->n, c0 = run->c0, end = run->end, h0 = run->h0, nh2 = run->nh2;
       const bool full = run->full;
       // ------------------------------------------------------------ copies
       if (lane == 0 && n > 0) {
@@ -864,32 +808,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tma_store_2d(&map_y, (h0 + b) * kP, run->begin + c * kQ, sb + L::kX + (k & 1) * 32768 + 16384u * b);
           tc::bulk_commit();
         };
-        load_x(c0, it);
-        load_b(c0);
-        if (full) load_c(c0);
 #pragma unroll 1
-        for (int j = 0; j < n && ok; ++j) {  // each buffer is loaded again as its last reader is done
+        for (int j = -1; j + 1 < n && ok; ++j) {  // chunk j + 1, each buffer as its last reader is done
           const int c = c0 + j;
           const uint32_t k = it + j, kf = itf + j;
           if (j > 0 && full) {
-            wait2(kBarY, kf - 1, 2);
+            wait2(kBarY, kf - 1);
             if (!ok) break;
             store_y(c - 1, k - 1);
+            tc::bulk_wait_read_all();
           }
-          if (j + 1 == n) break;
-          if (full) tc::bulk_wait_read_all();
           load_x(c + 1, k + 1);
-          if (full) {
-            wait(kBarYc, kf, 2);
-            if (!ok) break;
-            load_c(c + 1);
-          }
-          wait2(kBarSall, k, 2);
+          if (j >= 0 && full) wait(kBarYc, kf);
+          if (ok && full) load_c(c + 1);
+          if (j >= 0) wait2(kBarSall, k);
           if (ok) load_b(c + 1);
         }
-        if (full && ok) {
-          wait2(kBarY, itf + n - 1, 2);
-          if (ok && run->t0(n) <= end) store_y(c1 - 1, it + n - 1);  // a ragged chunk is written by the y group
+        for (int j = max(0, n - 2); j < n && full; ++j) {  // the last two chunks' y; a ragged one is written by the y group
+          wait2(kBarY, itf + j);
+          if (ok && run->t0(j + 1) <= end) store_y(c0 + j, it + j);
         }
         tc::bulk_wait_read_all();
       }
@@ -902,44 +839,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     // product of 128 x 128 x 16 takes 170-220 cycles to issue instead of the
     // 66 it takes to execute.
     // ----------------------------------------------------- products of y
-    const uint64_t dc = tc::desc_sw128(sb + L::kC, 16, 1024), db = tc::desc_sw128(sb + L::kB, 16, 1024),
+    const uint64_t dc = tc::desc_sw128(sb + L::kC, 16, 1024), db0 = tc::desc_sw128(sb + L::kB, 16, 1024),
                    dh = tc::desc_sw128(sb + L::kH, 16, 1024), dx0 = tc::desc_sw128(sb + L::kX, 16384, 1024);
     for (uint32_t r = 0; next(r); ++r) {
       const int n = run->full ? run->n : 0;
 #pragma unroll 1
       for (int j = 0; j < n && ok; ++j) {
         const uint32_t k = it + j, kf = itf + j;
-        wait(kBarB, k, 1);
-        wait(kBarC, kf, 1);
-        if (j > 0) wait2(kBarY, kf - 1, 2);  // the accumulators are read
-        if (!ok) break;
-        tc::fence_after();
-        if (tc::elect()) {
+        wait(kBarB, k);
+        wait(kBarC, kf);
+        if (j > 0) wait2(kBarY, kf - 1);  // the accumulators are read
 #pragma unroll 1
-          for (int kk = 0; kk < N / 16; ++kk) {
-            const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-            tc::mma(tmem + kG, dc + ko, db + ko, kId, kk > 0);
-          }
-          tc::commit(bar(kBarG));
-        }
-        __syncwarp();
-        arm(kBarG);
-        wait2(kBarH, k, 2);
-        if (!ok) break;
-        tc::fence_after();
-        if (tc::elect()) {
+        for (int e = 0; e < 2; ++e) {  // G = C B^T, then Yc = C H^T
+          if (e == 1) wait2(kBarH, k);
+          if (!ok) break;
+          tc::fence_after();
+          if (tc::elect()) {
+            const uint64_t db = e ? dh : db0;
+            const uint32_t to = tmem + kG + (kYc - kG) * e;
 #pragma unroll 1
-          for (int kk = 0; kk < N / 16; ++kk) {
-            const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-            tc::mma(tmem + kYc, dc + ko, dh + ko, kId, kk > 0);
+            for (int kk = 0; kk < N / 16; ++kk) {
+              const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+              tc::mma(to, dc + ko, db + ko, kId, kk > 0);
+            }
+            tc::commit(bar(kBarG + e));
           }
-          tc::commit(bar(kBarYc));
+          __syncwarp();
+          arm(kBarG + e);
         }
-        __syncwarp();
-        arm(kBarYc);
-        wait2(kBarX, k, 1);
-        wait(kBarM, kf, 2);
-        if (run->t0(j + 1) > run->end) wait2(kBarR, k, 2);  // a ragged chunk's x is cleared behind its end
+        wait2(kBarX, k);
+        wait(kBarM, kf);
+        if (run->t0(j + 1) > run->end) wait2(kBarR, k);  // a ragged chunk's x is cleared behind its end
         if (!ok) break;
         tc::fence_after();
         if (tc::elect()) {
@@ -962,11 +892,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int j = 0; j < n && ok; ++j) {
         const uint32_t k = it + j;
-        wait(kBarB, k, 1);
-        wait2(kBarH, k, 2);
+        wait(kBarB, k);
+        wait2(kBarH, k);
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
-          wait(kBarW + (q & 1), q >> 1, 2);
+          wait(kBarW + (q & 1), q >> 1);
           if (!ok) break;
           tc::fence_after();
           if (tc::elect()) {
@@ -987,8 +917,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!done()) break;
     }
   } else {
+    // ------------------- Delta and the decays of both heads; the next run
     for (uint32_t r = 0; next(r); ++r) {
-      runs.next(p, &s_run[(r + 1) & 1]);
+      const int n = run->n, nh2 = run->nh2;
+      // lane: tokens 4 lane .. + 3 of the chunk, so a block of 32 is 8 lanes
+      const int seg = lane & 7;
+#pragma unroll 1
+      for (int j = 0; j <= n; ++j) {
+        if (j == (n > 0)) s_runs.next(p, &s_run[(r + 1) & 1]);  // behind the first chunk's decays
+        if (j == n) break;
+        const uint32_t k = it + j;
+        Arrays& a = arr[k & 1];
+        const int t = run->t0(j) + 4 * lane, left = run->end - t;
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {
+          const int h = run->h0 + min(e, nh2 - 1);
+          const T* const dtg = static_cast<const T*>(p.dt) + h;
+          T raw[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) raw[i] = dtg[(int64_t)min(t + i, run->end - 1) * p.lddt];
+          if (e == 0) {  // the readers of this buffer, two chunks before
+            if (j > 1) wait2(kBarH, k - 1);
+            if (j > 1 && run->full) wait2(kBarY, itf + j - 2);
+          }
+          const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+          float d[4], in[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float v = Elt<T>::to_f(raw[i]) + bias;
+            d[i] = p.softplus ? softplus_f(v) : v;
+            if (i >= left || e >= nh2) d[i] = 0.f;
+            in[i] = fmaf(d[i], A2, i ? in[i - 1] : 0.f);
+          }
+          float before = in[3], after = in[3];
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) {
+            const float u = __shfl_up_sync(0xffffffffu, before, o), v = __shfl_down_sync(0xffffffffu, after, o);
+            if (seg >= o) before += u;
+            if (seg + o < 8) after += v;
+          }
+          if (seg == 7) a.tot[e][lane >> 3] = before;
+          float u = __shfl_up_sync(0xffffffffu, before, 1), v = __shfl_down_sync(0xffffffffu, after, 1);
+          if (seg == 0) u = 0.f;
+          if (seg == 7) v = 0.f;
+          const float s2 = d[3] * A2, s1 = fmaf(d[2], A2, s2), s0 = fmaf(d[1], A2, s1);
+          *reinterpret_cast<float4*>(a.pre[e] + 4 * lane) = make_float4(u + in[0], u + in[1], u + in[2], u + in[3]);
+          *reinterpret_cast<float4*>(a.dl[e] + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
+          *reinterpret_cast<float4*>(a.f[e] + 4 * lane) =
+              make_float4(ex2(v + s0) * d[0], ex2(v + s1) * d[1], ex2(v + s2) * d[2], ex2(v) * d[3]);
+        }
+        __syncwarp();
+        if (lane == 0) arrive(bar(kBarA + (k & 1)));
+      }
       if (!done()) break;
     }
   }
@@ -1011,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc::fence_before();
   __syncthreads();
-  if (tid == 0 && s_abort) atomicOr(&g_fault_prefill, (unsigned)s_abort);
+  if (!ok) atomicOr(&g_fault_prefill, 2u);
   if (warp == 0) {
     tc::fence_after();
     tc::tmem_dealloc(tmem, 512);

@@ -105,6 +105,19 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t lim
   return false;
 }
 
+// The same wait as a few instructions in one place (code that many warps walk
+// through once in a while has to fit the instruction cache).
+__device__ __forceinline__ bool wait_until(uint32_t bar, uint32_t parity, uint32_t limit) {
+  uint32_t n;
+  asm volatile(
+      "{\n .reg .pred p, q;\n mov.u32 %0, 0;\n"
+      "W: mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D;\n"
+      " add.u32 %0, %0, 1;\n setp.lt.u32 q, %0, %3;\n @q bra.uni W;\nD:\n}\n"
+      : "=&r"(n)
+      : "r"(bar), "r"(parity), "r"(limit)
+      : "memory");
+  return n < limit;
+}
 // Whether the phase with the given parity has completed; does not block.
 __device__ __forceinline__ bool test(uint32_t bar, uint32_t parity) {
   uint32_t done;
