@@ -172,7 +172,7 @@ struct Lay {
   static constexpr int kMax = kArr + 2 * 3104;        // unsigned [2]: largest |x| Delta of the chunk (fp16)
   static constexpr int kUn = kMax + 16;               // float [2][2]: 1 / the power of two of Xw (fp16), by chunk and head
   static constexpr int kBars = kUn + 16;              // mbarriers
-  static constexpr int kSlot = kBars + 176;  // TMEM base address  // TMEM base address
+  static constexpr int kSlot = kBars + 192;  // TMEM base address  // TMEM base address
   static constexpr int kBytes = kSlot + 16;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -205,8 +205,9 @@ enum : int {
   kBarM = 15,     // M is written
   kBarR = 16,     // [2] Xw's warps are done with x
   kBarH = 18,     // [2] the state copy is written and S is read: the next chunk's products may start
-  kBarY = 20,     // [2] y is in place of x, its accumulators are read
-  kNumBars = 22
+  kBarY = 20,     // [2] y is in place of x
+  kBarT = 22,     // y's accumulators are read
+  kNumBars = 23
 };
 
 __device__ __forceinline__ uint32_t swz(int r, int c) {
@@ -355,7 +356,7 @@ struct Runs {
   }
 };
 
-template <typename T, int N>
+template <typename T, int N, bool GATE>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const SsdPrefillParams p, int npairs, int blocks, const __grid_constant__ CUtensorMap map_x,
                       const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_c,
@@ -529,16 +530,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float e = ex2(between);  // from the start of the chunk to this row
         const f2_t e2 = pk2(e, e), D2 = pk2(Dh, Dh);
         const int64_t t = t0 + row;
-        const T* zg = p.z && mine && row < nval ? static_cast<const T*>(p.z) + t * p.ldz + h * kP : nullptr;
-        wait2(kBarX, k);
-        wait(kBarYc, kf);
-        wait2(kBarR, k);
-        wait(kBarYm, kf);
+        const T* zg = GATE && mine && row < nval ? static_cast<const T*>(p.z) + t * p.ldz + h * kP : nullptr;
+        wait2(kBarR, k);   // x has landed, and Xw's warps are done with it
+        wait(kBarYm, kf);  // and so is Yc, issued before
         tc::fence_after();
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
           float yc[16], ym[16];
           tc::ld32x32b_x16_pair(tmem + lane_base + kYc + 64 * hd + 16 * i, tmem + lane_base + kG + 64 * hd + 16 * i, yc, ym);
+          if (i == 3) signal(kBarT);  // the next chunk's products may start
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             uint4* at = reinterpret_cast<uint4*>(xs + swz(row, 2 * i + u));
@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               o[2 * v] = lo2(r);
               o[2 * v + 1] = hi2(r);
             }
-            if (zg) {
+            if (GATE && zg) {
               float zv[8];
               if (p.zvec) load8(zg + 16 * i + 8 * u, zv);
               else
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float dec = ex2(tot);
         if (full) wait(kBarYc, kf);  // C H^T is done with the state copy
         wait2(kBarSall, k);
-        wait2(kBarR, k);
+        if (!kBf16) wait2(kBarR, k);  // (Xw's scale)
         tc::fence_after();
         const f2_t dec2 = pk2(dec, dec), un2 = kBf16 ? 0 : pk2(sUn[2 * (k & 1) + hrow], sUn[2 * (k & 1) + hrow]);
         const bool more = j + 1 < n;
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t k = it + j, kf = itf + j;
         wait(kBarB, k);
         wait(kBarC, kf);
-        if (j > 0) wait2(kBarY, kf - 1);  // the accumulators are read
+        if (j > 0) wait(kBarT, kf - 1);  // the accumulators are read
 #pragma unroll 1
         for (int e = 0; e < 2; ++e) {  // G = C B^T, then Yc = C H^T
           if (e == 1) wait2(kBarH, k);
@@ -1000,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int pairs(const SsdPrefillParams& p) { return p.ngroups * ((p.nheads / p.ngroups + 1) / 2); }
 
-template <typename T, int N>
+template <typename T, int N, bool GATE>
 cudaError_t run(const SsdPrefillParams& p, cudaStream_t s) {
   CUtensorMap mx, mb, mc, my;
   std::memset(&my, 0, sizeof(my));
@@ -1019,7 +1019,7 @@ cudaError_t run(const SsdPrefillParams& p, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int smem = Lay<N>::kAlloc;
-  e = cudaFuncSetAttribute(prefill_tc_kernel<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = cudaFuncSetAttribute(prefill_tc_kernel<T, N, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
@@ -1031,12 +1031,13 @@ cudaError_t run(const SsdPrefillParams& p, cudaStream_t s) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<T, N>, p, npairs, blocks, mx, mb, mc, my);
+  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<T, N, GATE>, p, npairs, blocks, mx, mb, mc, my);
 }
 
 template <typename T>
 cudaError_t run_t(const SsdPrefillParams& p, cudaStream_t s) {
-  return p.dstate == 128 ? run<T, 128>(p, s) : run<T, 64>(p, s);
+  if (p.z) return p.dstate == 128 ? run<T, 128, true>(p, s) : run<T, 64, true>(p, s);
+  return p.dstate == 128 ? run<T, 128, false>(p, s) : run<T, 64, false>(p, s);
 }
 
 }  // namespace
