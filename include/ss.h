@@ -520,11 +520,11 @@ SS_API size_t ss_ssd_prefill_workspace_size(int64_t tokens, int64_t nseq, int64_
  *   x, y (tokens, nheads, headdim);  dt (tokens, nheads);
  *   B, C (tokens, ngroups, dstate);  z like x or NULL (no gate)      dtype bf16 or fp16
  *   A, D, dt_bias (nheads,) fp32; D, dt_bias may be NULL
- *   state (nslots, nheads, headdim, dstate) fp32 in/out, 16-byte aligned, or
+ *   state (nslots, nheads, headdim, dstate) fp32 in/out, or
  *   NULL: every sequence starts from zero and no end state is kept.
  * headdim 64, dstate 64 or 128 (else SS_ERR_UNSUPPORTED).  Rows of x, B and C
- * start on 16-byte boundaries (a multiple of 8 elements apart), y and the
- * workspace are 16- and 256-byte aligned (else SS_ERR_ALIGNMENT).
+ * start on 16-byte boundaries (a multiple of 8 elements apart); y is 16-byte,
+ * state 32-byte and the workspace 256-byte aligned (else SS_ERR_ALIGNMENT).
  */
 SS_API ss_status ss_ssd_prefill(int64_t tokens, int64_t nseq, int64_t nheads, int64_t headdim,
                                 int64_t ngroups, int64_t dstate, int dtype, const void* x, int64_t ldx,

@@ -1149,7 +1149,7 @@ ss_status ss_ssd_prefill(int64_t tokens, int64_t nseq, int64_t nheads, int64_t h
   if (y && !aligned(y, 16)) return fail(SS_ERR_ALIGNMENT, "%s: y not 16-byte aligned", fn);
   for (const void* q : {(const void*)A, (const void*)D, (const void*)dt_bias})
     if (q && !aligned(q, 4)) return fail(SS_ERR_ALIGNMENT, "%s: fp32 pointer %p not 4-byte aligned", fn, q);
-  if (state && !aligned(state, 16)) return fail(SS_ERR_ALIGNMENT, "%s: state not 16-byte aligned", fn);
+  if (state && !aligned(state, 32)) return fail(SS_ERR_ALIGNMENT, "%s: state not 32-byte aligned", fn);
   if (nseq == 0) return SS_OK;
   if (current_sm_count(&p.sms) != 0) return fail(SS_ERR_CUDA, "%s: cannot query the device", fn);
   const size_t need = ss::prefill_workspace(tokens, nseq, nheads, ngroups, dstate, p.sms);

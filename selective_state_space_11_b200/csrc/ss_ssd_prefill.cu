@@ -51,6 +51,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cstring>
 #include <type_traits>
 
@@ -97,7 +98,8 @@ __host__ __device__ inline PlanLayout plan_layout(int64_t nseq, int blocks, int 
   return l;
 }
 
-// Fewest chunks worth a block of its own.
+// A block for every unit or for every kMinRange chunks, whichever is more: a
+// cut inside a unit costs a handover of its state.
 constexpr int kMinRange = 4;
 
 __global__ void __launch_bounds__(1024) prefill_plan_kernel(const SsdPrefillParams p, int npairs, int blocks) {
@@ -137,8 +139,8 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(const SsdPrefillPara
     __syncthreads();
   }
   const long long units = prefix[nseq] * npairs;
-  const long long least = (units + kMinRange - 1) / kMinRange;
-  const long long used = least < blocks ? least : blocks;
+  const long long most = max((long long)nseq * npairs, (units + kMinRange - 1) / kMinRange);
+  const long long used = most < blocks ? most : blocks;
   for (int j = tid; j <= blocks; j += 1024) {
     Cut c{nseq, 0, 0, 0};
     if (j < used) {
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           unsigned char* const to = sm + L::kW + (q & 1) * 24576 + xh * 4096;
           // the products of the quarter before the last have read the buffer
           if (q > 1 || j > 0) wait(kBarS + (q & 1), q > 1 ? 0 : 1);
-#pragma unroll 1
+#pragma unroll 2
           for (int k4 = xc; k4 < xc + 4; ++k4) {
             const uint4 xv = *reinterpret_cast<const uint4*>(from + swz(32 * q + lane, k4));
             const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
@@ -924,7 +926,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seg = lane & 7;
 #pragma unroll 1
       for (int j = 0; j <= n; ++j) {
-        if (j == (n > 0)) s_runs.next(p, &s_run[(r + 1) & 1]);  // behind the first chunk's decays
+        if (j == (n > 0)) {  // behind the first chunk's decays
+          Run* const then = &s_run[(r + 1) & 1];
+          s_runs.next(p, then);
+          if (lane == 0 && then->n > 0) {  // bring what its first chunk waits for into L2
+            tc::tma_prefetch_2d(&map_x, then->h0 * kP, then->t0(0));
+            if (then->nh2 > 1) tc::tma_prefetch_2d(&map_x, then->h0 * kP + kP, then->t0(0));
+            if (then->from_slot && p.state && !(p.slots.fresh && p.slots.fresh[then->seq]))
+              tc::bulk_prefetch(p.state + ((size_t)then->slot * p.nheads + then->h0) * kP * N, then->nh2 * kP * N * 4);
+          }
+        }
         if (j == n) break;
         const uint32_t k = it + j;
         Arrays& a = arr[k & 1];
@@ -1044,8 +1055,8 @@ cudaError_t run_t(const SsdPrefillParams& p, cudaStream_t s) {
 
 int prefill_blocks(int64_t tokens, int64_t nseq, int npairs, int sms) {
   const int64_t units = (tokens / kQ + nseq) * npairs;  // at most this many chunks
-  const int64_t least = (units + kMinRange - 1) / kMinRange;
-  return (int)(least < sms ? (least < 1 ? 1 : least) : sms);
+  const int64_t most = std::max(nseq * npairs, (units + kMinRange - 1) / kMinRange);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, sms));
 }
 
 size_t prefill_workspace(int64_t tokens, int64_t nseq, int64_t nheads, int64_t ngroups, int64_t dstate, int sms) {
