@@ -852,10 +852,10 @@ void conv_tm_strips(int64_t tokens, int* strip, int* nstrip) {
   *nstrip = (int)((tokens + len - 1) / len);
 }
 
-// Backward blocks per column group: about four per SM of a 148-SM device in all.
+// Backward blocks per column group: about two per SM of a 148-SM device in all.
 int norm_blocks(int64_t rows, int64_t dim, int64_t group, int slots) {
   const int64_t ngroups = dim / group;
-  int64_t cap = 592 / ngroups;
+  int64_t cap = 296 / ngroups;
   if (cap < 1) cap = 1;
   const int64_t need = (rows + slots - 1) / slots;
   return (int)(need < cap ? need : cap);
@@ -903,7 +903,7 @@ ss_status ss_conv1d_tm_fwd(int64_t tokens, int64_t nseq, int64_t dim, int64_t wi
   p.y = {{(int)dim0, (int)dim1, (int)dim2}, {y0, y1, y2}};
   const int64_t v = 16 / (int64_t)es;
   const bool vec = vec_rows(x, ldx, es) && dim0 % v == 0 && dim1 % v == 0 && dim2 % v == 0 && vec_rows(y0, 0, es) &&
-                   vec_rows(y1, 0, es) && vec_rows(y2, 0, es);
+                   vec_rows(y1, 0, es) && vec_rows(y2, 0, es) && aligned(w, 16);
   if (launch_injected())
     return fail(SS_ERR_CUDA, "%s: launch failure injected by SS_FAIL_LAUNCH (nothing enqueued)", fn);
   cudaError_t e = ss::launch_conv_tm_fwd(p, static_cast<ss::DType>(dtype), vec, sms, static_cast<cudaStream_t>(stream));
@@ -953,7 +953,7 @@ ss_status ss_conv1d_tm_bwd(int64_t tokens, int64_t nseq, int64_t dim, int64_t wi
   p.dx = dx; p.lddx = lddx; p.dw = dw; p.dbias = dbias;
   p.part = static_cast<float*>(workspace);
   const bool vec = vec_rows(x, ldx, es) && vec_rows(dx, lddx, es) && dim0 % 4 == 0 && dim1 % 4 == 0 && dim2 % 4 == 0 &&
-                   vec_rows(dy0, 0, es) && vec_rows(dy1, 0, es) && vec_rows(dy2, 0, es);
+                   vec_rows(dy0, 0, es) && vec_rows(dy1, 0, es) && vec_rows(dy2, 0, es) && aligned(w, 16);
   if (launch_injected())
     return fail(SS_ERR_CUDA, "%s: launch failure injected by SS_FAIL_LAUNCH (nothing enqueued)", fn);
   cudaError_t e = ss::launch_conv_tm_bwd(p, static_cast<ss::DType>(dtype), vec, static_cast<cudaStream_t>(stream));
@@ -977,6 +977,8 @@ ss_status ss_gated_norm_fwd(int64_t rows, int64_t dim, int64_t group, int dtype,
   for (const void* q : {(const void*)w, (const void*)rstd})
     if (q && !aligned(q, 4)) return fail(SS_ERR_ALIGNMENT, "%s: fp32 pointer %p not 4-byte aligned", fn, q);
   if (rows == 0) return SS_OK;
+  int sms = 0;
+  if (current_sm_count(&sms) != 0) return fail(SS_ERR_CUDA, "%s: cannot query the device", fn);
   ss::NormParams p{};
   p.rows = rows; p.dim = (int)dim; p.group = (int)group; p.gate_last = gate_last ? 1 : 0;
   p.x = x; p.ldx = ldx; p.z = z; p.ldz = ldz; p.w = w; p.eps = eps; p.y = y; p.rstd = rstd;
@@ -984,20 +986,18 @@ ss_status ss_gated_norm_fwd(int64_t rows, int64_t dim, int64_t group, int dtype,
                    aligned(w, 16);
   if (launch_injected())
     return fail(SS_ERR_CUDA, "%s: launch failure injected by SS_FAIL_LAUNCH (nothing enqueued)", fn);
-  cudaError_t e = ss::launch_gated_norm(p, false, static_cast<ss::DType>(dtype), vec, static_cast<cudaStream_t>(stream));
+  ss::norm_shape((int)group, &p.warps, &p.slots);
+  cudaError_t e =
+      ss::launch_gated_norm(p, false, static_cast<ss::DType>(dtype), vec, sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(SS_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return SS_OK;
 }
 
 size_t ss_gated_norm_bwd_workspace_size(int64_t rows, int64_t dim, int64_t group) {
   if (check_norm("ss_gated_norm_bwd_workspace_size", rows, dim, group) != SS_OK) return (size_t)-1;
-  size_t parts = 0;
-  for (bool vec : {false, true}) {  // either layout of the rows
-    if (vec && group % 8) continue;
-    const int slots = ss::norm_slots((int)group, vec);
-    const size_t n = (size_t)norm_blocks(rows, dim, group, slots) * slots;
-    if (n > parts) parts = n;
-  }
+  int warps = 0, slots = 0;
+  ss::norm_shape((int)group, &warps, &slots);
+  const size_t parts = (size_t)norm_blocks(rows, dim, group, slots) * slots;
   return round_up(parts * dim * sizeof(float), 256);
 }
 
@@ -1031,10 +1031,11 @@ ss_status ss_gated_norm_bwd(int64_t rows, int64_t dim, int64_t group, int dtype,
   p.dx = dx; p.lddx = lddx; p.dz = dz; p.lddz = lddz; p.dw = dw; p.part = static_cast<float*>(workspace);
   const bool vec = group % 8 == 0 && vec_rows(x, ldx, es) && vec_rows(z, ldz, es) && vec_rows(dy, dim, es) &&
                    vec_rows(dx, lddx, es) && vec_rows(dz, lddz, es) && aligned(w, 16);
-  p.nblk = norm_blocks(rows, dim, group, ss::norm_slots((int)group, vec));
+  ss::norm_shape((int)group, &p.warps, &p.slots);
+  p.nblk = norm_blocks(rows, dim, group, p.slots);
   if (launch_injected())
     return fail(SS_ERR_CUDA, "%s: launch failure injected by SS_FAIL_LAUNCH (nothing enqueued)", fn);
-  cudaError_t e = ss::launch_gated_norm(p, true, static_cast<ss::DType>(dtype), vec, static_cast<cudaStream_t>(stream));
+  cudaError_t e = ss::launch_gated_norm(p, true, static_cast<ss::DType>(dtype), vec, 0, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(SS_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return SS_OK;
 }

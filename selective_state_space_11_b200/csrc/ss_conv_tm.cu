@@ -11,7 +11,8 @@
 // Both passes are bound by HBM: forward 2 + 2 bytes per element in bf16
 // against W FMAs and two SFU operations.  A thread owns V adjacent channels
 // (one 16-byte load a token) and walks a tile of tokens with the W-1 previous
-// inputs in registers, four tokens' loads in flight.
+// inputs in registers and the next kRing - 1 rows on their way to its own
+// shared-memory slots.
 //
 // Forward: tiles never straddle two sequences (ss_ragged.cuh), so only a
 // sequence's first tile needs the incoming window, and the threads that read
@@ -23,6 +24,8 @@
 // strip recomputes dpre for W-1 tokens behind it.  dw and dbias stay in
 // registers over the strip, go to one partial per strip, and a second kernel
 // sums the strips in order: no atomics, bitwise reproducible.
+#include <type_traits>
+
 #include "ss_device.cuh"
 #include "ss_internal.h"
 #include "ss_ragged.cuh"
@@ -32,6 +35,25 @@ namespace ss {
 static __device__ unsigned int g_fault_conv_tm = 0;
 
 namespace {
+
+// One of the two 16-bit elements of a word, and two elements as a word.
+template <typename T>
+__device__ __forceinline__ float word_f(uint32_t w, int hi) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    return __uint_as_float(hi ? w & 0xffff0000u : w << 16);
+  else
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(hi ? w >> 16 : w & 0xffffu)));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t word_of(float lo, float hi) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
 
 // V elements of a row as loaded: 16 bytes (V > 1) or one element.
 template <typename T, int V>
@@ -51,7 +73,10 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0u;
   }
-  __device__ __forceinline__ float at(int i) const { return Elt<T>::to_f(reinterpret_cast<const T*>(w)[i]); }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return word_f<T>(w[i >> 1], i & 1);
+  }
 };
 template <typename T>
 struct Raw<T, 1> {
@@ -66,15 +91,94 @@ __device__ __forceinline__ void store_v(T* p, const float (&f)[V]) {
     *p = Elt<T>::from_f(f[0]);
   } else {
     uint32_t w[V * sizeof(T) / 4];
-    T* e = reinterpret_cast<T*>(w);
 #pragma unroll
-    for (int i = 0; i < V; ++i) e[i] = Elt<T>::from_f(f[i]);
+    for (int i = 0; i < V * (int)sizeof(T) / 4; ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(f[i]);
+      else w[i] = word_of<T>(f[2 * i], f[2 * i + 1]);
+    }
     if constexpr (sizeof(w) == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   }
 }
 
-__device__ __forceinline__ float silu_f(float x) { return x * sigmoid_f(x); }
+// A thread's own rows on their way from global to shared memory: D rows of one
+// V-element vector per thread, copied asynchronously (cp.async) by the thread
+// that reads them, so that no barrier is needed and loads in flight cost no
+// registers.  Single elements (V == 1) are loaded when they are read.
+template <typename T, int V, int D>
+struct Ring {
+  static constexpr int kBytes = V * (int)sizeof(T);
+  unsigned char* slot;  // this thread's, in row 0
+  uint32_t pitch;       // bytes from row to row
+  __device__ __forceinline__ void start(unsigned char* base, int threads) {
+    slot = base + threadIdx.x * kBytes;
+    pitch = threads * kBytes;
+  }
+  __device__ __forceinline__ void put(int row, const T* p) const {
+    if constexpr (V > 1) {
+      const unsigned to = static_cast<unsigned>(__cvta_generic_to_shared(slot + (row & (D - 1)) * pitch));
+      if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(p) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to), "l"(p) : "memory");
+    }
+  }
+  __device__ __forceinline__ void get(int row, const T* p, Raw<T, V>& r) const {
+    if constexpr (V == 1) {
+      r.load(p);
+    } else if constexpr (kBytes == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(slot + (row & (D - 1)) * pitch);
+      r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(slot + (row & (D - 1)) * pitch);
+      r.w[0] = v.x; r.w[1] = v.y;
+    }
+  }
+};
+
+// Channels go through the arithmetic two at a time (packed fp32 pairs); of a
+// single channel the high half is idle.
+template <int V>
+constexpr int pairs() { return (V + 1) / 2; }
+template <typename T, int V>
+__device__ __forceinline__ f2_t pair_at(const Raw<T, V>& r, int i) {
+  if constexpr (V == 1) return pk2(r.at(0), 0.f);
+  else return pk2(r.at(2 * i), r.at(2 * i + 1));
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pairs(T* p, const f2_t (&f)[pairs<V>()]) {
+  float o[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = i & 1 ? hi2(f[i / 2]) : lo2(f[i / 2]);
+  store_v<T, V>(p, o);
+}
+__device__ __forceinline__ f2_t silu_2(f2_t x) {
+  const f2_t d = add2(pk2(1.f, 1.f), ex2_2(mul2(x, pk2(-kLog2e, -kLog2e))));
+  return mul2(x, pk2(rcp(lo2(d)), rcp(hi2(d))));
+}
+// The taps of V adjacent channels, w (dim, W): contiguous, 16 bytes at a time
+// where there is more than one channel (they are aligned then); and their biases.
+template <int V, int W>
+__device__ __forceinline__ void load_taps(const ConvTmParams& p, int c, f2_t (&wk)[W][pairs<V>()], f2_t (&bv)[pairs<V>()]) {
+  const float* w = p.w + (size_t)c * W;
+  float f[V * W];
+  if constexpr (V * W % 4 == 0 && V > 1) {
+#pragma unroll
+    for (int i = 0; i < V * W; i += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(w + i));
+      f[i] = v.x; f[i + 1] = v.y; f[i + 2] = v.z; f[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V * W; ++i) f[i] = __ldg(w + i);
+  }
+#pragma unroll
+  for (int i = 0; i < pairs<V>(); ++i) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) wk[k][i] = pk2(f[2 * i * W + k], V > 1 ? f[(2 * i + 1) % V * W + k] : 0.f);
+    bv[i] = p.bias ? pk2(p.bias[c + 2 * i], V > 1 ? p.bias[c + (2 * i + 1) % V] : 0.f) : pk2(0.f, 0.f);
+  }
+}
 
 // The piece that holds channel c, and c's place in it.
 struct PieceAt {
@@ -87,6 +191,8 @@ __device__ __forceinline__ PieceAt piece_at(const Pieces& y, int c) {
   if (i == 1 && c >= y.width[1]) { c -= y.width[1]; i = 2; }
   return {i == 0 ? y.p[0] : i == 1 ? y.p[1] : y.p[2], i == 0 ? y.width[0] : i == 1 ? y.width[1] : y.width[2], c};
 }
+
+constexpr int kRing = 8;  // rows in flight per thread
 
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(128) conv_tm_fwd_kernel(const ConvTmParams p, int tile) {
@@ -104,24 +210,32 @@ __global__ void __launch_bounds__(128) conv_tm_fwd_kernel(const ConvTmParams p, 
 
   constexpr int H = W > 1 ? W - 1 : 1;
   const T* __restrict__ x = static_cast<const T*>(p.x) + c;
-  float wk[W][V], bv[V], win[H][V];
+  const int e = min(rt.end, s + tile);
+  extern __shared__ __align__(16) unsigned char smem[];
+  Ring<T, V, kRing> ring;
+  ring.start(smem, blockDim.x);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bv[i] = p.bias ? p.bias[c + i] : 0.f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) wk[k][i] = p.w[(size_t)(c + i) * W + k];
-#pragma unroll
-    for (int k = 0; k < H; ++k) win[k][i] = 0.f;
+  for (int u = 0; u < kRing - 1; ++u) {
+    if (s + u < e) ring.put(u, x + (int64_t)(s + u) * p.ldx);
+    cp_async_commit();
   }
+  constexpr int NP = pairs<V>();
+  f2_t wk[W][NP], bv[NP], win[H][NP];
+  load_taps<V, W>(p, c, wk, bv);
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+#pragma unroll
+    for (int k = 0; k < H; ++k) win[k][i] = pk2(0.f, 0.f);
   const bool first = rt.k == 0;
   float* st = p.slots.count > 0 ? p.state + ((size_t)slot * p.dim + c) * (W - 1) : nullptr;
   if (W > 1) {
     if (first) {
       if (st && !(p.slots.fresh && p.slots.fresh[rt.seq])) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < NP; ++i)
 #pragma unroll
-          for (int k = 0; k < W - 1; ++k) win[k][i] = st[i * (W - 1) + k];
+          for (int k = 0; k < W - 1; ++k)
+            win[k][i] = pk2(st[2 * i * (W - 1) + k], V > 1 ? st[(2 * i + 1) % V * (W - 1) + k] : 0.f);
       }
     } else {
 #pragma unroll
@@ -129,7 +243,7 @@ __global__ void __launch_bounds__(128) conv_tm_fwd_kernel(const ConvTmParams p, 
         Raw<T, V> r;
         r.load(x + (int64_t)(s - (W - 1) + k) * p.ldx);
 #pragma unroll
-        for (int i = 0; i < V; ++i) win[k][i] = r.at(i);
+        for (int i = 0; i < NP; ++i) win[k][i] = pair_at(r, i);
       }
     }
   }
@@ -142,42 +256,38 @@ __global__ void __launch_bounds__(128) conv_tm_fwd_kernel(const ConvTmParams p, 
       r.zero();
       if (pos >= 0) r.load(x + (int64_t)(rt.begin + pos) * p.ldx);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float v = r.at(i);
+      for (int i = 0; i < NP; ++i) {
+        f2_t v = pair_at(r, i);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
+        for (int j = k; j < W - 1; ++j)
           if (pos < 0 && j == W - 1 + pos) v = win[j][i];
-        st[i * (W - 1) + k] = v;
+        st[2 * i * (W - 1) + k] = lo2(v);
+        if (V > 1) st[(2 * i + 1) % V * (W - 1) + k] = hi2(v);
       }
     }
   }
   const PieceAt at = piece_at(p.y, c);
   T* __restrict__ y = static_cast<T*>(at.p) + at.col;
-  const int e = min(rt.end, s + tile);
-  constexpr int U = 4;
-  for (int t = s; t < e; t += U) {
-    Raw<T, V> r[U];
+#pragma unroll 4
+  for (int t = s; t < e; ++t) {
+    if (t + kRing - 1 < e) ring.put(t - s + kRing - 1, x + (int64_t)(t + kRing - 1) * p.ldx);
+    cp_async_commit();
+    cp_async_wait_group<kRing - 1>();
+    Raw<T, V> r;
+    ring.get(t - s, x + (int64_t)t * p.ldx, r);
+    f2_t o[NP];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (t + u < e) r[u].load(x + (int64_t)(t + u) * p.ldx);
-      else r[u].zero();
+    for (int i = 0; i < NP; ++i) {
+      const f2_t xv = pair_at(r, i);
+      o[i] = fma2(wk[W - 1][i], xv, bv[i]);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (t + u >= e) break;
-      float o[V];
+      for (int k = 0; k < W - 1; ++k) o[i] = fma2(wk[k][i], win[k][i], o[i]);
+      if (p.silu) o[i] = silu_2(o[i]);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float xv = r[u].at(i);
-        float pre = fmaf(wk[W - 1][i], xv, bv[i]);
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k) pre = fmaf(wk[k][i], win[k][i], pre);
-        o[i] = p.silu ? silu_f(pre) : pre;
-#pragma unroll
-        for (int k = 0; k + 1 < W - 1; ++k) win[k][i] = win[k + 1][i];
-        if (W > 1) win[H - 1][i] = xv;
-      }
-      store_v<T, V>(y + (int64_t)(t + u) * at.width, o);
+      for (int k = 0; k + 1 < W - 1; ++k) win[k][i] = win[k + 1][i];
+      if (W > 1) win[H - 1][i] = xv;
     }
+    store_pairs<T, V>(y + (int64_t)t * at.width, o);
   }
 }
 
@@ -208,7 +318,7 @@ struct Walk {
   }
 };
 
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool SILU>
 __global__ void __launch_bounds__(128) conv_tm_bwd_kernel(const ConvTmParams p) {
   if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, &g_fault_conv_tm);
   const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
@@ -219,18 +329,28 @@ __global__ void __launch_bounds__(128) conv_tm_bwd_kernel(const ConvTmParams p) 
   const PieceAt at = piece_at(p.y, c);
   const T* __restrict__ dy = static_cast<const T*>(at.p) + at.col;
   T* __restrict__ dx = static_cast<T*>(p.dx) + c;
-  float wk[W][V], bv[V], win[H][V], dp[W][V], dwk[W][V], dbv[V];
+  const int last = min(p.seq.tokens, e + W - 1);  // tokens whose dpre the strip needs
+  extern __shared__ __align__(16) unsigned char smem[];
+  Ring<T, V, kRing> ringx, ringg;
+  ringx.start(smem, blockDim.x);
+  ringg.start(smem + kRing * blockDim.x * V * sizeof(T), blockDim.x);
+#pragma unroll
+  for (int u = 0; u < kRing - 1; ++u) {
+    if (s + u < last) {
+      ringx.put(u, x + (int64_t)(s + u) * p.ldx);
+      ringg.put(u, dy + (int64_t)(s + u) * at.width);
+    }
+    cp_async_commit();
+  }
+  constexpr int NP = pairs<V>();
+  f2_t wk[W][NP], bv[NP], win[H][NP], dp[W][NP], dwk[W][NP], dbv[NP];
+  load_taps<V, W>(p, c, wk, bv);
   int ps[W];  // positions of tokens t-(W-1) .. t, or -1
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bv[i] = p.bias ? p.bias[c + i] : 0.f;
-    dbv[i] = 0.f;
+  for (int i = 0; i < NP; ++i) {
+    dbv[i] = pk2(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-      wk[k][i] = p.w[(size_t)(c + i) * W + k];
-      dwk[k][i] = 0.f;
-      dp[k][i] = 0.f;
-    }
+    for (int k = 0; k < W; ++k) dwk[k][i] = dp[k][i] = pk2(0.f, 0.f);
   }
 #pragma unroll
   for (int k = 0; k < W; ++k) ps[k] = -1;
@@ -241,77 +361,88 @@ __global__ void __launch_bounds__(128) conv_tm_bwd_kernel(const ConvTmParams p) 
     const int t = s - H + k;
     if (W > 1 && t >= 0) r.load(x + (int64_t)t * p.ldx);
 #pragma unroll
-    for (int i = 0; i < V; ++i) win[k][i] = r.at(i);
+    for (int i = 0; i < NP; ++i) win[k][i] = pair_at(r, i);
   }
   Walk walk;
   walk.start(p.seq, s);
-  const int last = min(p.seq.tokens, e + W - 1);  // tokens whose dpre the strip needs
-  constexpr int U = 2;
-  for (int t = s; t < e + W - 1; t += U) {
-    Raw<T, V> rx[U], rg[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      rx[u].zero();
-      rg[u].zero();
-      if (t + u < last) {
-        rx[u].load(x + (int64_t)(t + u) * p.ldx);
-        rg[u].load(dy + (int64_t)(t + u) * at.width);
-      }
+#pragma unroll 4
+  for (int tt = s; tt < e + W - 1; ++tt) {
+    const int n = tt + kRing - 1;
+    if (n < last) {
+      ringx.put(n - s, x + (int64_t)n * p.ldx);
+      ringg.put(n - s, dy + (int64_t)n * at.width);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int tt = t + u;
-      if (tt >= e + W - 1) break;
-      const int pos = tt < last ? walk.pos(p.seq, tt) : -1;
-#pragma unroll
-      for (int k = 0; k + 1 < W; ++k) ps[k] = ps[k + 1];
-      ps[W - 1] = pos;
-      const bool own = tt < e;  // else only dx of earlier tokens needs this dpre
-      float dxv[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float xv = rx[u].at(i);
-        float tap[W];
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k) tap[k] = pos >= W - 1 - k ? win[k][i] : 0.f;
-        tap[W - 1] = xv;
-        float pre = bv[i];
-#pragma unroll
-        for (int k = 0; k < W; ++k) pre = fmaf(wk[k][i], tap[k], pre);
-        float d = rg[u].at(i);
-        if (p.silu) {
-          const float sg = sigmoid_f(pre);
-          d *= sg * fmaf(pre, 1.f - sg, 1.f);
-        }
-        if (pos < 0) d = 0.f;  // a token of no sequence
-        if (own && pos >= 0) {
-          dbv[i] += d;
-#pragma unroll
-          for (int k = 0; k < W; ++k) dwk[k][i] = fmaf(d, tap[k], dwk[k][i]);
-        }
-#pragma unroll
-        for (int k = 0; k + 1 < W; ++k) dp[k][i] = dp[k + 1][i];
-        dp[W - 1][i] = d;
-        // dx of token tt-(W-1): the dpre of the m-th token after it, where that is of the same sequence
-        float a = 0.f;
-#pragma unroll
-        for (int m = 0; m < W; ++m)
-          if (ps[0] >= 0 && ps[m] >= m) a = fmaf(wk[W - 1 - m][i], dp[m][i], a);
-        dxv[i] = a;
-#pragma unroll
-        for (int k = 0; k + 1 < W - 1; ++k) win[k][i] = win[k + 1][i];
-        if (W > 1) win[H - 1][i] = xv;
-      }
-      const int td = tt - (W - 1);
-      if (td >= s) store_v<T, V>(dx + (int64_t)td * p.lddx, dxv);
+    cp_async_commit();
+    cp_async_wait_group<kRing - 1>();
+    const bool there = tt < last;
+    Raw<T, V> rx, rg;
+    rx.zero();
+    rg.zero();
+    if (there) {
+      ringx.get(tt - s, x + (int64_t)tt * p.ldx, rx);
+      ringg.get(tt - s, dy + (int64_t)tt * at.width, rg);
     }
+    const int pos = there ? walk.pos(p.seq, tt) : -1;
+#pragma unroll
+    for (int k = 0; k + 1 < W; ++k) ps[k] = ps[k + 1];
+    ps[W - 1] = pos;
+    const bool own = tt < e;  // else only dx of earlier tokens needs this dpre
+    // From its W-th token on, all taps of a token, and all tokens that dx of
+    // token tt-(W-1) takes, are of the token's own sequence: nothing to mask.
+    const f2_t zero = pk2(0.f, 0.f), one = pk2(1.f, 1.f);
+    f2_t dxv[NP];
+    auto token = [&](auto plain) {
+      constexpr bool kPlain = decltype(plain)::value;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      f2_t tap[W];
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k) tap[k] = win[k][i];
+      tap[W - 1] = pair_at(rx, i);
+      if (!kPlain)
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+          if (pos < W - 1 - k) tap[k] = zero;
+      f2_t pre = bv[i];
+#pragma unroll
+      for (int k = 0; k < W; ++k) pre = fma2(wk[k][i], tap[k], pre);
+      f2_t d = pair_at(rg, i);
+      if (SILU) {
+        const f2_t den = add2(one, ex2_2(mul2(pre, pk2(-kLog2e, -kLog2e))));
+        const f2_t sg = pk2(rcp(lo2(den)), rcp(hi2(den)));
+        d = mul2(d, mul2(sg, fma2(pre, fma2(sg, pk2(-1.f, -1.f), one), one)));
+      }
+      if (!kPlain && pos < 0) d = zero;  // a token of no sequence
+      if (kPlain || (own && pos >= 0)) {
+        dbv[i] = add2(dbv[i], d);
+#pragma unroll
+        for (int k = 0; k < W; ++k) dwk[k][i] = fma2(d, tap[k], dwk[k][i]);
+      }
+#pragma unroll
+      for (int k = 0; k + 1 < W; ++k) dp[k][i] = dp[k + 1][i];
+      dp[W - 1][i] = d;
+      // dx of token tt-(W-1): the dpre of the m-th token after it, where that is of the same sequence
+      f2_t a = zero;
+#pragma unroll
+      for (int m = 0; m < W; ++m)
+        if (kPlain || (ps[0] >= 0 && ps[m] >= m)) a = fma2(wk[W - 1 - m][i], dp[m][i], a);
+      dxv[i] = a;
+#pragma unroll
+      for (int k = 0; k + 1 < W - 1; ++k) win[k][i] = win[k + 1][i];
+      if (W > 1) win[H - 1][i] = pair_at(rx, i);
+    }
+    };
+    if (own && pos >= W - 1) token(std::true_type{});
+    else token(std::false_type{});
+    const int td = tt - (W - 1);
+    if (td >= s) store_pairs<T, V>(dx + (int64_t)td * p.lddx, dxv);
   }
   float* part = p.part + ((size_t)blockIdx.x * p.dim + c) * (W + 1);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
 #pragma unroll
-    for (int k = 0; k < W; ++k) part[i * (W + 1) + k] = dwk[k][i];
-    part[i * (W + 1) + W] = dbv[i];
+    for (int k = 0; k < W; ++k) part[i * (W + 1) + k] = i & 1 ? hi2(dwk[k][i / 2]) : lo2(dwk[k][i / 2]);
+    part[i * (W + 1) + W] = i & 1 ? hi2(dbv[i / 2]) : lo2(dbv[i / 2]);
   }
 }
 
@@ -357,14 +488,16 @@ cudaError_t run(const ConvTmParams& p, bool backward, int sms, cudaStream_t s) {
   const unsigned ny = (nvec + nt - 1) / nt;
   if (!backward) {
     // longer tiles re-read less (W-1 rows each); shorter ones keep every SM busy on few tokens
-    int tile = 64;
+    int tile = 32;
     while (tile > 8 && (long long)(p.seq.tokens / tile) * ny * nt < (long long)sms * 1024) tile /= 2;
     const long long tiles = ragged_tiles(p.seq, tile);
-    conv_tm_fwd_kernel<T, V, W><<<dim3((unsigned)tiles, ny), nt, 0, s>>>(p, tile);
+    conv_tm_fwd_kernel<T, V, W><<<dim3((unsigned)tiles, ny), nt, V > 1 ? kRing * nt * V * sizeof(T) : 0, s>>>(p, tile);
     return cudaGetLastError();
   }
   if (p.nstrip > 0) {
-    conv_tm_bwd_kernel<T, V, W><<<dim3((unsigned)p.nstrip, ny), nt, 0, s>>>(p);
+    const size_t smem = V > 1 ? 2 * kRing * nt * V * sizeof(T) : 0;
+    if (p.silu) conv_tm_bwd_kernel<T, V, W, true><<<dim3((unsigned)p.nstrip, ny), nt, smem, s>>>(p);
+    else conv_tm_bwd_kernel<T, V, W, false><<<dim3((unsigned)p.nstrip, ny), nt, smem, s>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -388,7 +521,7 @@ cudaError_t run_w(const ConvTmParams& p, bool backward, int sms, cudaStream_t s)
 template <typename T>
 cudaError_t run_t(const ConvTmParams& p, bool backward, bool vec, int sms, cudaStream_t s) {
   if (!vec) return run_w<T, 1>(p, backward, sms, s);
-  return backward ? run_w<T, 4>(p, true, sms, s) : run_w<T, 16 / sizeof(T)>(p, false, sms, s);
+  return backward ? run_w<T, 4>(p, true, sms, s) : run_w<T, 4>(p, false, sms, s);
 }
 
 cudaError_t dispatch(const ConvTmParams& p, bool backward, DType dt, bool vec, int sms, cudaStream_t s) {

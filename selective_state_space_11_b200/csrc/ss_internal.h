@@ -215,6 +215,7 @@ struct NormParams {
   int64_t lddx, lddz;
   float* dw;                  // (dim,)
   float* part;                // backward workspace: (parts, dim)
+  int warps, slots;           // warps per group, groups per block (norm_shape)
   int nblk;                   // backward: blocks per group
 };
 
@@ -247,10 +248,10 @@ struct SsdPrefillParams {
 
 cudaError_t launch_conv_tm_fwd(const ConvTmParams& p, DType dt, bool vec, int sms, cudaStream_t s);
 cudaError_t launch_conv_tm_bwd(const ConvTmParams& p, DType dt, bool vec, cudaStream_t s);
-// Column groups (of `group` columns, 16-byte vectors or not) that a block of the norm holds at once.
-int norm_slots(int group, bool vec);
+// Warps per column group of the norm, and groups that a block holds at once.
+void norm_shape(int group, int* warps, int* slots);
 constexpr int kMaxNormGroup = 8192;
-cudaError_t launch_gated_norm(const NormParams& p, bool backward, DType dt, bool vec, cudaStream_t s);
+cudaError_t launch_gated_norm(const NormParams& p, bool backward, DType dt, bool vec, int sms, cudaStream_t s);
 cudaError_t launch_ssd_step(const SsdStepParams& p, DType dt, cudaStream_t s);
 // Persistent blocks of the prefill, and its workspace, on a device of `sms` SMs.
 int prefill_blocks(int64_t tokens, int64_t nseq, int npairs, int sms);

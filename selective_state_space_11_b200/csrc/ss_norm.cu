@@ -13,191 +13,237 @@
 //   gate last:  dx = dv,       dz = dy n w s'(z)
 // with s'(z) = sigmoid(z) (1 + z (1 - sigmoid(z))).
 //
-// Bound by HBM: forward 3 arrays, backward 5.  A row's group lives in
-// registers between the sum and the output, so each array moves once.  WPR
-// warps share a group (several groups per 256-thread block when it is
-// small); their sums meet in shared memory in a fixed order.  The backward
-// walks rows with dw in registers, writes one partial row per walker, and a
-// second kernel sums those in order: no atomics.  All sums are fp32.
+// Bound by HBM: forward 3 arrays, backward 5.  A thread holds 8 columns of a
+// group, so a group of G columns takes ceil(G / 256) warps and a block as many
+// groups as fill 20 warps; the group's sum meets in shared memory, in a fixed
+// order.  Blocks walk their rows, and a row's loads are under way while the row
+// before is summed and written: each array moves once, and HBM does not wait
+// for the block's barrier.  The backward keeps w and dw in registers over its
+// rows, writes one partial row per walker, and a second kernel sums those in
+// order: no atomics, bitwise reproducible.  All sums are fp32.
+#include <type_traits>
+
 #include "ss_device.cuh"
 #include "ss_internal.h"
 
 namespace ss {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kE = 8;  // columns per thread
 
-// K vectors of V elements per thread of a group's WPR warps: vector i of the
-// thread is vector t + i * WPR * 32 of the group.
-template <typename T, int V>
-struct Vec {
-  float f[V];
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (V == 8) load8(p, f);
-    else f[0] = ldf(p);
+// A thread's columns of one row, as loaded.  Vector rows: 8 adjacent ones (16
+// or 32 bytes); others: single ones, a group's threads apart.
+template <typename T, bool VEC>
+struct Cols {
+  static constexpr int kWords = kE * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* row, int t, int nt, int n) {
+    if constexpr (VEC) {
+      if (t * kE < n) {
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + t * kE) + i);
+          w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        }
+        return;
+      }
+      zero();
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) w[i] = t + i * nt < n ? __ldg(reinterpret_cast<const uint32_t*>(row) + t + i * nt) : 0u;
+    } else {
+      const unsigned short* r = reinterpret_cast<const unsigned short*>(row);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t a = t + 2 * i * nt < n ? __ldg(r + t + 2 * i * nt) : 0u;
+        const uint32_t b = t + (2 * i + 1) * nt < n ? __ldg(r + t + (2 * i + 1) * nt) : 0u;
+        w[i] = a | (b << 16);
+      }
+    }
   }
-  __device__ __forceinline__ void store(T* p) const {
-    if constexpr (V == 8) store8(p, f);
-    else stf(p, f[0]);
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ f2_t pair(int i) const {
+    if constexpr (std::is_same<T, __half>::value) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      return pk2(f.x, f.y);
+    } else {
+      return pk2(at(2 * i), at(2 * i + 1));
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    else
+      return __half2float(__ushort_as_half(static_cast<unsigned short>(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu)));
   }
 };
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_cols(T* row, int t, int nt, int n, const float (&f)[kE]) {
+  if constexpr (VEC) {
+    if (t * kE < n) store8(row + t * kE, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kE; ++i)
+      if (t + i * nt < n) stf(row + t + i * nt, f[i]);
+  }
+}
 
-// Sum over the WPR warps of a group; every thread gets it.  `sh` holds one
+__device__ __forceinline__ f2_t sigmoid_2(f2_t x) {
+  const f2_t d = add2(pk2(1.f, 1.f), ex2_2(mul2(x, pk2(-kLog2e, -kLog2e))));
+  return pk2(rcp(lo2(d)), rcp(hi2(d)));
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_pairs(T* row, int t, int nt, int n, const f2_t (&f)[kE / 2]) {
+  float o[kE];
+#pragma unroll
+  for (int i = 0; i < kE; ++i) o[i] = i & 1 ? hi2(f[i / 2]) : lo2(f[i / 2]);
+  store_cols<T, VEC>(row, t, nt, n, o);
+}
+
+// Sum over the `warps` warps of a group; every thread gets it.  `sh` holds a
 // float per warp; the caller alternates two of them between calls.
-template <int WPR>
-__device__ __forceinline__ float group_sum(float v, float* sh) {
+__device__ __forceinline__ float group_sum(float v, float* sh, int warps) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (WPR == 1) return v;
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) sh[warp] = v;
+  if (warps == 1) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) sh[warp] = v;
   __syncthreads();
-  float a = 0.f;
+  v = lane < warps ? sh[warp / warps * warps + lane] : 0.f;
 #pragma unroll
-  for (int i = 0; i < WPR; ++i) a += sh[warp / WPR * WPR + i];
-  return a;
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
-template <typename T, int V, int K, int WPR>
-__global__ void __launch_bounds__(kThreads) norm_fwd_kernel(const NormParams p) {
-  __shared__ float sh[kWarps];
-  constexpr int kSlots = kWarps / WPR;
-  const int ngroups = p.dim / p.group;
-  const int64_t item = (int64_t)blockIdx.x * kSlots + threadIdx.x / (32 * WPR);
-  const bool live = item < p.rows * ngroups;
-  const int64_t row = live ? item / ngroups : 0;
-  const int g = live ? (int)(item - row * ngroups) : 0;
-  const int t = threadIdx.x % (32 * WPR);
-  const int nvec = p.group / V;
-  const int c0 = g * p.group;
-  const T* x = static_cast<const T*>(p.x) + row * p.ldx + c0;
-  const T* z = p.z ? static_cast<const T*>(p.z) + row * p.ldz + c0 : nullptr;
-  Vec<T, V> v[K], gt[K];
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const int j = t + i * WPR * 32;
-    if (live && j < nvec) {
-      v[i].load(x + j * V);
-      if (z) gt[i].load(z + j * V);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) v[i].f[e] = gt[i].f[e] = 0.f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < K; ++i)
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      if (z) {
-        gt[i].f[e] *= sigmoid_f(gt[i].f[e]);
-        if (!p.gate_last) v[i].f[e] *= gt[i].f[e];
-      }
-      ss = fmaf(v[i].f[e], v[i].f[e], ss);
-    }
-  ss = group_sum<WPR>(ss, sh);
-  if (!live) return;
-  const float rstd = rsqrtf(ss / p.group + p.eps);
-  T* y = static_cast<T*>(p.y) + row * p.dim + c0;
-#pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const int j = t + i * WPR * 32;
-    if (j >= nvec) break;
-    Vec<float, V> w;
-    w.load(p.w + c0 + j * V);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      float o = v[i].f[e] * rstd * w.f[e];
-      if (z && p.gate_last) o *= gt[i].f[e];
-      v[i].f[e] = o;
-    }
-    v[i].store(y + j * V);
-  }
-  if (p.rstd && t == 0) p.rstd[item] = rstd;
-}
-
-template <typename T, int V, int K, int WPR>
-__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormParams p) {
-  __shared__ float sh[2][kWarps];
-  constexpr int kSlots = kWarps / WPR;
-  const int ngroups = p.dim / p.group;
-  const int g = blockIdx.y;
-  const int walker = blockIdx.x * kSlots + threadIdx.x / (32 * WPR);
-  const int t = threadIdx.x % (32 * WPR);
-  const int nvec = p.group / V;
-  const int c0 = g * p.group;
-  const int64_t step = (int64_t)p.nblk * kSlots;
-  Vec<float, V> w[K], dw[K];
-#pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const int j = t + i * WPR * 32;
-#pragma unroll
-    for (int e = 0; e < V; ++e) w[i].f[e] = dw[i].f[e] = 0.f;
-    if (j < nvec) w[i].load(p.w + c0 + j * V);
-  }
+// GATE: there is a z; LAST: its gate multiplies the normalised row.
+template <typename T, bool VEC, int THREADS, bool GATE, bool LAST>
+__global__ void __launch_bounds__(THREADS, THREADS == 640 ? 2 : 1) norm_fwd_kernel(const NormParams p) {
+  __shared__ float sh[2][32];
+  const int nt = p.warps * 32, slot = threadIdx.x / nt, t = threadIdx.x - slot * nt, n = p.group;
+  const int ngroups = p.dim / n;
+  const int64_t items = p.rows * ngroups, step = (int64_t)gridDim.x * p.slots;
+  Cols<T, VEC> x, z, ax, az;  // this row's, and the next one's on their way
+  auto fetch = [&](int64_t item) {
+    ax.zero();
+    az.zero();
+    if (item >= items) return;
+    const int64_t row = ngroups == 1 ? item : item / ngroups;
+    const int c0 = (int)(item - row * ngroups) * n;
+    ax.load(static_cast<const T*>(p.x) + row * p.ldx + c0, t, nt, n);
+    if (GATE) az.load(static_cast<const T*>(p.z) + row * p.ldz + c0, t, nt, n);
+  };
+  fetch((int64_t)blockIdx.x * p.slots + slot);
   int flip = 0;
-  // every slot of the block makes the same number of turns (the sum holds a block barrier)
-  for (int64_t r0 = (int64_t)blockIdx.x * kSlots; r0 < p.rows; r0 += step, flip ^= 1) {
-    const int64_t row = r0 + threadIdx.x / (32 * WPR);
-    const bool live = row < p.rows;
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx + c0;
-    const T* z = p.z ? static_cast<const T*>(p.z) + row * p.ldz + c0 : nullptr;
-    const T* dy = static_cast<const T*>(p.dy) + row * p.dim + c0;
-    Vec<T, V> vx[K], vz[K], vd[K];
+  // every slot of a block makes the same number of turns (the sum holds a block barrier)
+  for (int64_t base = (int64_t)blockIdx.x * p.slots; base < items; base += step, flip ^= 1) {
+    const int64_t item = base + slot;
+    x = ax;
+    z = az;
+    fetch(item + step);
+    f2_t v[kE / 2], gate[kE / 2], sq = pk2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
-      const int j = t + i * WPR * 32;
-#pragma unroll
-      for (int e = 0; e < V; ++e) vx[i].f[e] = vz[i].f[e] = vd[i].f[e] = 0.f;
-      if (live && j < nvec) {
-        vx[i].load(x + j * V);
-        vd[i].load(dy + j * V);
-        if (z) vz[i].load(z + j * V);
+    for (int i = 0; i < kE / 2; ++i) {
+      v[i] = x.pair(i);
+      if (GATE) {
+        gate[i] = mul2(z.pair(i), sigmoid_2(z.pair(i)));
+        if (!LAST) v[i] = mul2(v[i], gate[i]);
       }
+      sq = fma2(v[i], v[i], sq);
     }
-    const float rstd = live ? p.rstd[row * ngroups + g] : 0.f;
-    float c = 0.f;
+    const float ss = group_sum(lo2(sq) + hi2(sq), sh[flip], p.warps);
+    if (item >= items) continue;
+    const float rstd = rsqrtf(ss / n + p.eps);
+    const int64_t row = ngroups == 1 ? item : item / ngroups;
+    const int c0 = (int)(item - row * ngroups) * n;
+    Cols<float, VEC> w;
+    w.load(p.w + c0, t, nt, n);
+    const f2_t rstd2 = pk2(rstd, rstd);
 #pragma unroll
-    for (int i = 0; i < K; ++i)
+    for (int i = 0; i < kE / 2; ++i) {
+      v[i] = mul2(mul2(v[i], rstd2), w.pair(i));
+      if (GATE && LAST) v[i] = mul2(v[i], gate[i]);
+    }
+    store_pairs<T, VEC>(static_cast<T*>(p.y) + row * p.dim + c0, t, nt, n, v);
+    if (p.rstd && t == 0) p.rstd[item] = rstd;
+  }
+}
+
+// GATE: there is a z; LAST: its gate multiplies the normalised row.
+template <typename T, bool VEC, int THREADS, bool GATE, bool LAST>
+__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormParams p) {
+  __shared__ float sh[2][32];
+  const int nt = p.warps * 32, slot = threadIdx.x / nt, t = threadIdx.x - slot * nt, n = p.group;
+  const int g = blockIdx.y, ngroups = gridDim.y, c0 = g * n;
+  const int64_t step = (int64_t)p.nblk * p.slots;
+  Cols<float, VEC> w;
+  w.load(p.w + c0, t, nt, n);
+  f2_t dw[kE / 2];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float zv = vz[i].f[e], sg = sigmoid_f(zv);
-        const float gate = z ? zv * sg : 1.f;
-        const float n = (p.gate_last ? vx[i].f[e] : vx[i].f[e] * gate) * rstd;
-        const float q = p.gate_last ? vd[i].f[e] * gate : vd[i].f[e];
-        dw[i].f[e] = fmaf(q, n, dw[i].f[e]);
-        c = fmaf(q * w[i].f[e], n, c);
+  for (int i = 0; i < kE / 2; ++i) dw[i] = pk2(0.f, 0.f);
+  Cols<T, VEC> x, z, d, ax, az, ad;
+  float rstd = 0.f, arstd = 0.f;
+  auto fetch = [&](int64_t row) {
+    ax.zero();
+    az.zero();
+    ad.zero();
+    arstd = 0.f;
+    if (row >= p.rows) return;
+    ax.load(static_cast<const T*>(p.x) + row * p.ldx + c0, t, nt, n);
+    if (GATE) az.load(static_cast<const T*>(p.z) + row * p.ldz + c0, t, nt, n);
+    ad.load(static_cast<const T*>(p.dy) + row * p.dim + c0, t, nt, n);
+    arstd = p.rstd[row * ngroups + g];
+  };
+  fetch((int64_t)blockIdx.x * p.slots + slot);
+  int flip = 0;
+  for (int64_t base = (int64_t)blockIdx.x * p.slots; base < p.rows; base += step, flip ^= 1) {
+    const int64_t row = base + slot;
+    x = ax;
+    z = az;
+    d = ad;
+    rstd = arstd;
+    fetch(row + step);
+    const f2_t rstd2 = pk2(rstd, rstd), one = pk2(1.f, 1.f), minus = pk2(-1.f, -1.f);
+    f2_t sg[kE / 2], nv[kE / 2], dn[kE / 2], sum = pk2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kE / 2; ++i) {
+      f2_t q = d.pair(i);
+      nv[i] = mul2(x.pair(i), rstd2);
+      if (GATE) {
+        sg[i] = sigmoid_2(z.pair(i));
+        const f2_t gate = mul2(z.pair(i), sg[i]);
+        if (LAST) q = mul2(q, gate);
+        else nv[i] = mul2(nv[i], gate);
       }
-    c = group_sum<WPR>(c, sh[flip]) / p.group;
-    if (live) {
-      T* dx = static_cast<T*>(p.dx) + row * p.lddx + c0;
-      T* dz = z ? static_cast<T*>(p.dz) + row * p.lddz + c0 : nullptr;
+      dw[i] = fma2(q, nv[i], dw[i]);
+      dn[i] = mul2(q, w.pair(i));
+      sum = fma2(dn[i], nv[i], sum);
+    }
+    const float c = group_sum(lo2(sum) + hi2(sum), sh[flip], p.warps) / n;
+    if (row >= p.rows) continue;
+    const f2_t c2 = pk2(-c, -c);
+    f2_t ox[kE / 2], oz[kE / 2];
 #pragma unroll
-      for (int i = 0; i < K; ++i) {
-        const int j = t + i * WPR * 32;
-        if (j >= nvec) break;
-        Vec<T, V> ox, oz;
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float zv = vz[i].f[e], sg = sigmoid_f(zv);
-          const float gate = z ? zv * sg : 1.f, dgate = sg * fmaf(zv, 1.f - sg, 1.f);
-          const float n = (p.gate_last ? vx[i].f[e] : vx[i].f[e] * gate) * rstd;
-          const float dn = (p.gate_last ? vd[i].f[e] * gate : vd[i].f[e]) * w[i].f[e];
-          const float dv = rstd * fmaf(-n, c, dn);
-          ox.f[e] = p.gate_last ? dv : dv * gate;
-          oz.f[e] = (p.gate_last ? vd[i].f[e] * n * w[i].f[e] : dv * vx[i].f[e]) * dgate;
+    for (int i = 0; i < kE / 2; ++i) {
+      ox[i] = mul2(rstd2, fma2(nv[i], c2, dn[i]));  // dv
+      if (GATE) {
+        const f2_t zv = z.pair(i), dgate = mul2(sg[i], fma2(zv, fma2(sg[i], minus, one), one));
+        if (LAST) {
+          oz[i] = mul2(mul2(d.pair(i), w.pair(i)), mul2(nv[i], dgate));
+        } else {
+          oz[i] = mul2(mul2(ox[i], x.pair(i)), dgate);
+          ox[i] = mul2(ox[i], mul2(zv, sg[i]));
         }
-        ox.store(dx + j * V);
-        if (z) oz.store(dz + j * V);
       }
     }
+    store_pairs<T, VEC>(static_cast<T*>(p.dx) + row * p.lddx + c0, t, nt, n, ox);
+    if (GATE) store_pairs<T, VEC>(static_cast<T*>(p.dz) + row * p.lddz + c0, t, nt, n, oz);
   }
-  float* part = p.part + (size_t)walker * p.dim + c0;
-#pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const int j = t + i * WPR * 32;
-    if (j < nvec) dw[i].store(part + j * V);
-  }
+  float* part = p.part + (size_t)(blockIdx.x * p.slots + slot) * p.dim + c0;
+  store_pairs<float, VEC>(part, t, nt, n, dw);
 }
 
 __global__ void __launch_bounds__(256) norm_reduce_kernel(const NormParams p, int parts) {
@@ -215,58 +261,56 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const NormParams p, in
   p.dw[j] = a;
 }
 
-template <typename T, int V, int K, int WPR>
-cudaError_t run(const NormParams& p, bool backward, cudaStream_t s) {
-  constexpr int kSlots = kWarps / WPR;
+template <typename T, bool VEC, int THREADS, bool GATE, bool LAST>
+cudaError_t run(const NormParams& p, bool backward, int sms, cudaStream_t s) {
   const int ngroups = p.dim / p.group;
   if (!backward) {
-    const int64_t blocks = (p.rows * ngroups + kSlots - 1) / kSlots;
-    norm_fwd_kernel<T, V, K, WPR><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    NormParams q = p;
+    const int64_t items = p.rows * ngroups;
+    while (q.slots > 1 && items < (int64_t)sms * q.slots) --q.slots;  // few rows: spread them over the SMs
+    const int threads = q.slots * q.warps * 32;
+    const int64_t need = (items + q.slots - 1) / q.slots, most = (int64_t)sms * (1280 / threads > 0 ? 1280 / threads : 1);
+    norm_fwd_kernel<T, VEC, THREADS, GATE, LAST><<<(unsigned)(need < most ? need : most), threads, 0, s>>>(q);
     return cudaGetLastError();
   }
+  const int threads = p.slots * p.warps * 32;
   if (p.nblk > 0) {
-    norm_bwd_kernel<T, V, K, WPR><<<dim3(p.nblk, ngroups), kThreads, 0, s>>>(p);
+    norm_bwd_kernel<T, VEC, THREADS, GATE, LAST><<<dim3(p.nblk, ngroups), threads, 0, s>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  norm_reduce_kernel<<<(p.dim + 31) / 32, 256, 0, s>>>(p, p.nblk * kSlots);
+  norm_reduce_kernel<<<(p.dim + 31) / 32, 256, 0, s>>>(p, p.nblk * p.slots);
   return cudaGetLastError();
 }
 
-// Warps per group and vectors per thread: the fewest warps whose threads hold
-// at most two vectors each, all eight (and more vectors) for wide groups.
-template <typename T, int V>
-cudaError_t run_shape(const NormParams& p, bool backward, cudaStream_t s) {
-  const int nvec = p.group / V;
-  if (nvec <= 32) return run<T, V, 1, 1>(p, backward, s);
-  if (nvec <= 64) return run<T, V, 2, 1>(p, backward, s);
-  if (nvec <= 128) return run<T, V, 2, 2>(p, backward, s);
-  if (nvec <= 256) return run<T, V, 2, 4>(p, backward, s);
-  if (nvec <= 512) return run<T, V, 2, 8>(p, backward, s);
-  if (nvec <= 768) return run<T, V, 3, 8>(p, backward, s);
-  if (nvec <= 1024) return run<T, V, 4, 8>(p, backward, s);
-  if (V == 1 && nvec <= 8192) return run<T, V, V == 1 ? 32 : 1, 8>(p, backward, s);
-  return cudaErrorInvalidValue;
+template <typename T, bool VEC, int THREADS>
+cudaError_t run_g(const NormParams& p, bool backward, int sms, cudaStream_t s) {
+  if (!p.z) return run<T, VEC, THREADS, false, false>(p, backward, sms, s);
+  return p.gate_last ? run<T, VEC, THREADS, true, true>(p, backward, sms, s)
+                     : run<T, VEC, THREADS, true, false>(p, backward, sms, s);
 }
-
+template <typename T, bool VEC>
+cudaError_t run_v(const NormParams& p, bool backward, int sms, cudaStream_t s) {
+  // wide groups need the threads of a whole block and have half the registers each
+  return p.slots * p.warps <= 20 ? run_g<T, VEC, 640>(p, backward, sms, s) : run_g<T, VEC, 1024>(p, backward, sms, s);
+}
 template <typename T>
-cudaError_t run_t(const NormParams& p, bool backward, bool vec, cudaStream_t s) {
-  return vec ? run_shape<T, 8>(p, backward, s) : run_shape<T, 1>(p, backward, s);
+cudaError_t run_t(const NormParams& p, bool backward, bool vec, int sms, cudaStream_t s) {
+  return vec ? run_v<T, true>(p, backward, sms, s) : run_v<T, false>(p, backward, sms, s);
 }
 
 }  // namespace
 
-// Groups a block holds at once (as run_shape picks them).
-int norm_slots(int group, bool vec) {
-  const int nvec = vec ? group / 8 : group;
-  return nvec <= 64 ? 8 : nvec <= 128 ? 4 : nvec <= 256 ? 2 : 1;
+void norm_shape(int group, int* warps, int* slots) {
+  *warps = (group + 32 * kE - 1) / (32 * kE);
+  *slots = *warps >= 20 ? 1 : 20 / *warps;
 }
 
-cudaError_t launch_gated_norm(const NormParams& p, bool backward, DType dt, bool vec, cudaStream_t s) {
+cudaError_t launch_gated_norm(const NormParams& p, bool backward, DType dt, bool vec, int sms, cudaStream_t s) {
   switch (dt) {
-    case DType::F32: return run_t<float>(p, backward, vec, s);
-    case DType::BF16: return run_t<__nv_bfloat16>(p, backward, vec, s);
-    case DType::F16: return run_t<__half>(p, backward, vec, s);
+    case DType::F32: return run_t<float>(p, backward, vec, sms, s);
+    case DType::BF16: return run_t<__nv_bfloat16>(p, backward, vec, sms, s);
+    case DType::F16: return run_t<__half>(p, backward, vec, sms, s);
   }
   return cudaErrorInvalidValue;
 }
