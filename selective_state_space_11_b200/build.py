@@ -11,6 +11,8 @@ import argparse
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -46,9 +48,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc()] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + [
-        "-shared", "-o", tmp] + [os.path.join(CSRC, f) for f in SOURCES]
-    subprocess.check_call(cmd, cwd=CSRC)
+    flags = NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else [])
+    with tempfile.TemporaryDirectory() as objs:
+        def compile_one(src: str) -> str:
+            obj = os.path.join(objs, src + ".o")
+            subprocess.check_call([_nvcc()] + flags + ["-c", "-o", obj, os.path.join(CSRC, src)], cwd=CSRC)
+            return obj
+
+        with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:  # each file is an nvcc process of its own
+            made = list(pool.map(compile_one, SOURCES))
+        subprocess.check_call([_nvcc()] + NVCC_FLAGS + ["-shared", "-o", tmp] + made, cwd=CSRC)
     os.replace(tmp, LIB)
     return LIB
 

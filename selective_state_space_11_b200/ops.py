@@ -540,9 +540,48 @@ def ssd_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, dt_softplus=True, 
 
 
 # ---- time-major operators around the SSD scan (Mamba-2) ---------------------
+# A decode step of a small model is a few microseconds of GPU time, so these
+# checks take the common case with few calls into torch.
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _is(t: Optional[torch.Tensor], name: str, shape, dtype, dev, optional=False):
+    if t is None and optional:
+        return
+    if t is not None and t.is_cuda and t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous():
+        return
+    _need(t, name, shape, dtype, dev, optional)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+class _On:
+    """The device of the tensors, made current while the library is called; yields its current stream."""
+
+    def __init__(self, dev):
+        self.dev = dev
+        self.ctx = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return _raw_stream(self.dev.index) if _raw_stream else torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
 def _need_rows(t: torch.Tensor, name: str, lead, tail, dtype, dev) -> int:
     """Check a tensor of shape lead + tail whose rows (the tail) are contiguous and
     evenly spaced along the lead axes; returns the distance between rows in elements."""
+    if t is not None and t.is_cuda and t.dtype is dtype and t.device == dev and t.shape == lead + tail:
+        if len(lead) == 1:
+            width, stride = tail[0] * (tail[1] if len(tail) == 2 else 1), t.stride()
+            if stride[-1] == 1 and stride[0] >= width and lead[0] > 1 and (len(tail) == 1 or stride[1] == tail[1]):
+                return stride[0]
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
@@ -584,15 +623,15 @@ def _ragged(lead, cu_seqlens, dev) -> Tuple[int, int]:
         return lead[0], 1
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens has one offset per sequence and the end")
-    _need(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, dev)
+    _is(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, dev)
     return lead[0], cu_seqlens.numel() - 1
 
 
 def _slot_args(nseq, slots, fresh, dev):
-    _need(slots, "slots", (nseq,), torch.int32, dev, optional=True)
+    _is(slots, "slots", (nseq,), torch.int32, dev, optional=True)
     if fresh is not None and fresh.dtype == torch.bool:
         fresh = fresh.view(torch.uint8)
-    _need(fresh, "fresh", (nseq,), torch.uint8, dev, optional=True)
+    _is(fresh, "fresh", (nseq,), torch.uint8, dev, optional=True)
     return fresh
 
 
@@ -604,7 +643,7 @@ def _ws(need: int, workspace, dev):
         return None
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         return torch.empty(need, device=dev, dtype=torch.uint8)
-    _need(workspace, "workspace", workspace.shape, workspace.dtype, dev)
+    _is(workspace, "workspace", workspace.shape, workspace.dtype, dev)
     return workspace
 
 
@@ -616,8 +655,8 @@ def _check_conv_tm(x, w, bias, splits, cu_seqlens):
     dev, lead, dim, W = x.device, tuple(x.shape[:-1]), x.shape[-1], w.shape[-1]
     ldx = _need_rows(x, "x", lead, (dim,), x.dtype, dev)
     tokens, nseq = _ragged(lead, cu_seqlens, dev)
-    _need(w, "w", (dim, W), torch.float32, dev)
-    _need(bias, "bias", (dim,), torch.float32, dev, optional=True)
+    _is(w, "w", (dim, W), torch.float32, dev)
+    _is(bias, "bias", (dim,), torch.float32, dev, optional=True)
     splits = (dim,) if splits is None else tuple(int(s) for s in splits)
     if not 1 <= len(splits) <= 3 or sum(splits) != dim or min(splits) <= 0:
         raise ValueError(f"splits {splits}: one to three positive widths that sum to {dim}")
@@ -641,7 +680,7 @@ def conv1d_tm_fwd(x, w, bias=None, splits=None, cu_seqlens=None, state=None, slo
     nslots = 0
     if state is not None:
         nslots = state.shape[0]
-        _need(state, "state", (nslots, dim, W - 1), torch.float32, dev)
+        _is(state, "state", (nslots, dim, W - 1), torch.float32, dev)
     elif slots is not None or fresh is not None:
         raise ValueError("slots and fresh go with a state cache")
     fresh = _slot_args(nseq, slots, fresh, dev)
@@ -650,13 +689,13 @@ def conv1d_tm_fwd(x, w, bias=None, splits=None, cu_seqlens=None, state=None, slo
     if len(out) != len(splits):
         raise ValueError(f"out holds {len(out)} pieces, expected {len(splits)}")
     for i, (o, s) in enumerate(zip(out, splits)):
-        _need(o, f"out[{i}]", lead + (s,), x.dtype, dev)
+        _is(o, f"out[{i}]", lead + (s,), x.dtype, dev)
     d = splits + (0,) * (3 - len(splits))
     y = tuple(out) + (None,) * (3 - len(splits))
-    with torch.cuda.device(dev):
-        _check(lib().ss_conv1d_tm_fwd(tokens, nseq, dim, W, _DTYPE[x.dtype], _ptr(x), ldx, _ptr(w), _ptr(bias),
-                                      _ptr(cu_seqlens), _ptr(state), nslots, _ptr(slots), _ptr(fresh),
-                                      int(bool(silu)), *d, *map(_ptr, y), _stream(dev)))
+    with _On(dev) as stream:
+        _check(lib().ss_conv1d_tm_fwd(tokens, nseq, dim, W, _DTYPE[x.dtype], _at(x), ldx, _at(w), _at(bias),
+                                      _at(cu_seqlens), _at(state), nslots, _at(slots), _at(fresh),
+                                      int(bool(silu)), *d, *map(_at, y), stream))
     return tuple(out)
 
 
@@ -670,7 +709,7 @@ def conv1d_tm_bwd(x, w, dy, bias=None, cu_seqlens=None, silu=True, dx=None,
     """
     dev, lead, tokens, nseq, dim, W, ldx, splits = _check_conv_tm(x, w, bias, [t.shape[-1] for t in dy], cu_seqlens)
     for i, (t, s) in enumerate(zip(dy, splits)):
-        _need(t, f"dy[{i}]", lead + (s,), x.dtype, dev)
+        _is(t, f"dy[{i}]", lead + (s,), x.dtype, dev)
     if dx is None:
         dx = torch.empty(*lead, dim, device=dev, dtype=x.dtype)
     lddx = _need_rows(dx, "dx", lead, (dim,), x.dtype, dev)
@@ -678,12 +717,12 @@ def conv1d_tm_bwd(x, w, dy, bias=None, cu_seqlens=None, silu=True, dx=None,
     g = dict(dx=dx, dw=torch.empty(dim, W, **f32), dbias=torch.empty(dim, **f32))
     d = splits + (0,) * (3 - len(splits))
     t = tuple(dy) + (None,) * (3 - len(splits))
-    with torch.cuda.device(dev):
+    with _On(dev) as stream:
         workspace = _ws(lib().ss_conv1d_tm_bwd_workspace_size(tokens, dim, W), workspace, dev)
         size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib().ss_conv1d_tm_bwd(tokens, nseq, dim, W, _DTYPE[x.dtype], _ptr(x), ldx, _ptr(w), _ptr(bias),
-                                      _ptr(cu_seqlens), int(bool(silu)), *d, *map(_ptr, t), _ptr(dx), lddx,
-                                      _ptr(g["dw"]), _ptr(g["dbias"]), _ptr(workspace), size, _stream(dev)))
+        _check(lib().ss_conv1d_tm_bwd(tokens, nseq, dim, W, _DTYPE[x.dtype], _at(x), ldx, _at(w), _at(bias),
+                                      _at(cu_seqlens), int(bool(silu)), *d, *map(_at, t), _at(dx), lddx,
+                                      _at(g["dw"]), _at(g["dbias"]), _at(workspace), size, stream))
     return g
 
 
@@ -729,25 +768,25 @@ def ssd_prefill(x, dt, A, B, C, state=None, D=None, z=None, dt_bias=None, dt_sof
     ldb = _need_rows(B, "B", lead, (ng, N), x.dtype, dev)
     ldc = _need_rows(C, "C", lead, (ng, N), x.dtype, dev)
     ldz = 0 if z is None else _need_rows(z, "z", lead, (nh, P), x.dtype, dev)
-    _need(A, "A", (nh,), torch.float32, dev)
-    _need(D, "D", (nh,), torch.float32, dev, optional=True)
-    _need(dt_bias, "dt_bias", (nh,), torch.float32, dev, optional=True)
+    _is(A, "A", (nh,), torch.float32, dev)
+    _is(D, "D", (nh,), torch.float32, dev, optional=True)
+    _is(dt_bias, "dt_bias", (nh,), torch.float32, dev, optional=True)
     nslots = 0
     if state is not None:
         nslots = state.shape[0]
-        _need(state, "state", (nslots, nh, P, N), torch.float32, dev)
+        _is(state, "state", (nslots, nh, P, N), torch.float32, dev)
     elif slots is not None or fresh is not None:
         raise ValueError("slots and fresh go with a state cache")
     fresh = _slot_args(nseq, slots, fresh, dev)
     y = out if out is not None else torch.empty(*lead, nh, P, device=dev, dtype=x.dtype)
-    _need(y, "out", lead + (nh, P), x.dtype, dev)
-    with torch.cuda.device(dev):
+    _is(y, "out", lead + (nh, P), x.dtype, dev)
+    with _On(dev) as stream:
         workspace = _ws(lib().ss_ssd_prefill_workspace_size(tokens, nseq, nh, P, ng, N), workspace, dev)
         size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib().ss_ssd_prefill(tokens, nseq, nh, P, ng, N, _DTYPE[x.dtype], _ptr(x), ldx, _ptr(dt), lddt,
-                                    _ptr(A), _ptr(B), ldb, _ptr(C), ldc, _ptr(D), _ptr(z), ldz, _ptr(dt_bias),
-                                    int(bool(dt_softplus)), _ptr(cu_seqlens), _ptr(state), nslots, _ptr(slots),
-                                    _ptr(fresh), _ptr(y), _ptr(workspace), size, _stream(dev)))
+        _check(lib().ss_ssd_prefill(tokens, nseq, nh, P, ng, N, _DTYPE[x.dtype], _at(x), ldx, _at(dt), lddt,
+                                    _at(A), _at(B), ldb, _at(C), ldc, _at(D), _at(z), ldz, _at(dt_bias),
+                                    int(bool(dt_softplus)), _at(cu_seqlens), _at(state), nslots, _at(slots),
+                                    _at(fresh), _at(y), _at(workspace), size, stream))
     return y
 
 
@@ -772,23 +811,23 @@ def ssd_step(xbc, dt, w, A, conv_state, state, conv_bias=None, D=None, z=None, d
     ldx = _need_rows(xbc, "xbc", (bsz,), (dim,), xbc.dtype, dev)
     lddt = _need_rows(dt, "dt", (bsz,), (nh,), xbc.dtype, dev)
     ldz = 0 if z is None else _need_rows(z, "z", (bsz,), (nh * P,), xbc.dtype, dev)
-    _need(w, "w", (dim, W), torch.float32, dev)
-    _need(conv_bias, "conv_bias", (dim,), torch.float32, dev, optional=True)
-    _need(A, "A", (nh,), torch.float32, dev)
-    _need(D, "D", (nh,), torch.float32, dev, optional=True)
-    _need(dt_bias, "dt_bias", (nh,), torch.float32, dev, optional=True)
-    _need(conv_state, "conv_state", (nslots, dim, W - 1), torch.float32, dev)
-    _need(state, "state", (nslots, nh, P, N), torch.float32, dev)
+    _is(w, "w", (dim, W), torch.float32, dev)
+    _is(conv_bias, "conv_bias", (dim,), torch.float32, dev, optional=True)
+    _is(A, "A", (nh,), torch.float32, dev)
+    _is(D, "D", (nh,), torch.float32, dev, optional=True)
+    _is(dt_bias, "dt_bias", (nh,), torch.float32, dev, optional=True)
+    _is(conv_state, "conv_state", (nslots, dim, W - 1), torch.float32, dev)
+    _is(state, "state", (nslots, nh, P, N), torch.float32, dev)
     _slot_args(bsz, slots, None, dev)
     y = out if out is not None else torch.empty(bsz, nh, P, device=dev, dtype=xbc.dtype)
-    _need(y, "out", (bsz, nh, P), xbc.dtype, dev)
-    with torch.cuda.device(dev):
+    _is(y, "out", (bsz, nh, P), xbc.dtype, dev)
+    with _On(dev) as stream:
         workspace = _ws(lib().ss_ssd_step_workspace_size(bsz, nh, P, ngroups, N), workspace, dev)
         size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib().ss_ssd_step(bsz, nh, P, ngroups, N, W, _DTYPE[xbc.dtype], _ptr(xbc), ldx, _ptr(dt), lddt,
-                                 _ptr(w), _ptr(conv_bias), int(bool(silu)), _ptr(A), _ptr(D), _ptr(z), ldz,
-                                 _ptr(dt_bias), int(bool(dt_softplus)), _ptr(conv_state), _ptr(state), nslots,
-                                 _ptr(slots), _ptr(y), _ptr(workspace), size, _stream(dev)))
+        _check(lib().ss_ssd_step(bsz, nh, P, ngroups, N, W, _DTYPE[xbc.dtype], _at(xbc), ldx, _at(dt), lddt,
+                                 _at(w), _at(conv_bias), int(bool(silu)), _at(A), _at(D), _at(z), ldz,
+                                 _at(dt_bias), int(bool(dt_softplus)), _at(conv_state), _at(state), nslots,
+                                 _at(slots), _at(y), _at(workspace), size, stream))
     return y
 
 
@@ -800,7 +839,7 @@ def _check_norm(x, z, w, group):
     dev, lead, dim = x.device, tuple(x.shape[:-1]), x.shape[-1]
     ldx = _need_rows(x, "x", lead, (dim,), x.dtype, dev)
     ldz = 0 if z is None else _need_rows(z, "z", lead, (dim,), x.dtype, dev)
-    _need(w, "w", (dim,), torch.float32, dev)
+    _is(w, "w", (dim,), torch.float32, dev)
     group = dim if group is None else int(group)
     if group <= 0 or dim % group:
         raise ValueError(f"group={group} must divide dim={dim}")
@@ -820,11 +859,11 @@ def gated_norm_fwd(x, z, w, group=None, eps=1e-5, gate_last=False, want_rstd=Tru
     """
     dev, lead, rows, dim, group, ldx, ldz = _check_norm(x, z, w, group)
     y = out if out is not None else torch.empty(*lead, dim, device=dev, dtype=x.dtype)
-    _need(y, "out", lead + (dim,), x.dtype, dev)
+    _is(y, "out", lead + (dim,), x.dtype, dev)
     rstd = torch.empty(*lead, dim // group, device=dev, dtype=torch.float32) if want_rstd else None
-    with torch.cuda.device(dev):
-        _check(lib().ss_gated_norm_fwd(rows, dim, group, _DTYPE[x.dtype], _ptr(x), ldx, _ptr(z), ldz, _ptr(w),
-                                       float(eps), int(bool(gate_last)), _ptr(y), _ptr(rstd), _stream(dev)))
+    with _On(dev) as stream:
+        _check(lib().ss_gated_norm_fwd(rows, dim, group, _DTYPE[x.dtype], _at(x), ldx, _at(z), ldz, _at(w),
+                                       float(eps), int(bool(gate_last)), _at(y), _at(rstd), stream))
     return y, rstd
 
 
@@ -834,8 +873,8 @@ def gated_norm_bwd(x, z, w, dy, rstd, group=None, gate_last=False, dx=None, dz=N
     dtype and dw (dim,) fp32.  ``dx`` and ``dz`` may be supplied, also as column
     slices of a wider gradient."""
     dev, lead, rows, dim, group, ldx, ldz = _check_norm(x, z, w, group)
-    _need(dy, "dy", lead + (dim,), x.dtype, dev)
-    _need(rstd, "rstd", lead + (dim // group,), torch.float32, dev)
+    _is(dy, "dy", lead + (dim,), x.dtype, dev)
+    _is(rstd, "rstd", lead + (dim // group,), torch.float32, dev)
     if z is None and dz is not None:
         raise ValueError("dz given without z")
     new = dict(device=dev, dtype=x.dtype)
@@ -844,12 +883,12 @@ def gated_norm_bwd(x, z, w, dy, rstd, group=None, gate_last=False, dx=None, dz=N
     lddx = _need_rows(dx, "dx", lead, (dim,), x.dtype, dev)
     lddz = 0 if dz is None else _need_rows(dz, "dz", lead, (dim,), x.dtype, dev)
     dw = torch.empty(dim, device=dev, dtype=torch.float32)
-    with torch.cuda.device(dev):
+    with _On(dev) as stream:
         workspace = _ws(lib().ss_gated_norm_bwd_workspace_size(rows, dim, group), workspace, dev)
         size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib().ss_gated_norm_bwd(rows, dim, group, _DTYPE[x.dtype], _ptr(x), ldx, _ptr(z), ldz, _ptr(w),
-                                       _ptr(rstd), _ptr(dy), int(bool(gate_last)), _ptr(dx), lddx, _ptr(dz), lddz,
-                                       _ptr(dw), _ptr(workspace), size, _stream(dev)))
+        _check(lib().ss_gated_norm_bwd(rows, dim, group, _DTYPE[x.dtype], _at(x), ldx, _at(z), ldz, _at(w),
+                                       _at(rstd), _at(dy), int(bool(gate_last)), _at(dx), lddx, _at(dz), lddz,
+                                       _at(dw), _at(workspace), size, stream))
     return dict(dx=dx, dz=dz, dw=dw)
 
 
