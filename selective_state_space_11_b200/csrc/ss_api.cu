@@ -836,7 +836,8 @@ ss_status check_conv_tm(const char* fn, int64_t dim, int64_t width, int dtype, i
   if (st != SS_OK) return st;
   if (width < 1 || width > 4)
     return fail(SS_ERR_UNSUPPORTED, "%s: width=%lld (supported: 1..4)", fn, (long long)width);
-  if (dim <= 0 || dim0 <= 0 || dim1 < 0 || dim2 < 0 || (dim1 == 0 && dim2 > 0) || dim0 + dim1 + dim2 != dim)
+  if (dim <= 0 || dim0 <= 0 || dim1 < 0 || dim2 < 0 || (dim1 == 0 && dim2 > 0) || dim0 > dim || dim1 > dim - dim0 ||
+      dim2 != dim - dim0 - dim1)
     return fail(SS_ERR_INVALID_ARG, "%s: dim=%lld must be the sum of its pieces (%lld, %lld, %lld), empty ones last",
                 fn, (long long)dim, (long long)dim0, (long long)dim1, (long long)dim2);
   if (dim > (1 << 22)) return fail(SS_ERR_UNSUPPORTED, "%s: dim above 2^22", fn);

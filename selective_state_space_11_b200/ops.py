@@ -729,7 +729,10 @@ def conv1d_tm_bwd(x, w, dy, bias=None, cu_seqlens=None, silu=True, dx=None,
 class _CausalConv1dTm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, splits, cu_seqlens, silu):
-        y = conv1d_tm_fwd(x, w, bias, splits=splits, cu_seqlens=cu_seqlens, silu=silu)
+        out = None
+        if cu_seqlens is not None:  # rows of no sequence are not written: zero, as their gradient is
+            out = tuple(x.new_zeros(*x.shape[:-1], s) for s in splits or (x.shape[-1],))
+        y = conv1d_tm_fwd(x, w, bias, splits=splits, cu_seqlens=cu_seqlens, silu=silu, out=out)
         ctx.save_for_backward(x, w, bias, cu_seqlens)
         ctx.silu = silu
         return y
@@ -742,7 +745,8 @@ class _CausalConv1dTm(torch.autograd.Function):
 
 
 def causal_conv1d_tm_fn(x, w, bias=None, splits=None, cu_seqlens=None, silu=True):
-    """Differentiable conv1d_tm_fwd (no cache): a tuple of pieces; x (tokens, dim) or (batch, L, dim)."""
+    """Differentiable conv1d_tm_fwd (no cache): a tuple of pieces; x (tokens, dim) or
+    (batch, L, dim).  Rows of no sequence are zero, and so are their gradients."""
     return _CausalConv1dTm.apply(x, w, bias, splits, cu_seqlens, silu)
 
 
