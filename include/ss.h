@@ -472,6 +472,8 @@ SS_API ss_status ss_state_update(int64_t batch, int64_t dim, int64_t dstate, int
  *     calls capture into CUDA graphs, and a replay follows the data then in
  *     cu_seqlens, slots and fresh.
  *   - A NaN or an infinity in one sequence never reaches another's results.
+ *   - Outputs do not overlap inputs, but for the in/out caches.
+ *   - Nothing outside the rows and slots in use is written.
  *   - Sizes: tokens < 2^31 - 2^16, nseq <= 65536, batch <= 65535; tokens, nseq,
  *     rows and batch may be 0.
  */
@@ -525,6 +527,15 @@ SS_API size_t ss_ssd_prefill_workspace_size(int64_t tokens, int64_t nseq, int64_
  * headdim 64, dstate 64 or 128 (else SS_ERR_UNSUPPORTED).  Rows of x, B and C
  * start on 16-byte boundaries (a multiple of 8 elements apart); y is 16-byte,
  * state 32-byte and the workspace 256-byte aligned (else SS_ERR_ALIGNMENT).
+ * The state is accurate to fp32.  y takes one 16-bit rounding of the masked
+ * products (C_i . B_j) decay Delta_j and of the state entering a run of 128
+ * tokens, on top of its own: in fp16 these overflow, in y alone, above 65504.
+ * Decays are meant to be at most 1 (A <= 0, Delta >= 0); growth works until
+ * fp32 overflows inside 128 tokens.  A NaN or an infinity in x, B, C or dt of a token may
+ * reach y of up to 127 tokens before it in its own sequence (one tile of the
+ * tensor cores); earlier and other sequences' tokens are never reached.
+ * Waits inside the kernel are bounded: one that runs out sets bits 1 or 2 of
+ * ss_device_fault.
  */
 SS_API ss_status ss_ssd_prefill(int64_t tokens, int64_t nseq, int64_t nheads, int64_t headdim,
                                 int64_t ngroups, int64_t dstate, int dtype, const void* x, int64_t ldx,

@@ -14,14 +14,23 @@
 //   H <- exp(cs_last) H + Xw^T B,   Xw_t = exp(cs_last - cs_t) Delta_t x_t
 //   y  = (Y + D x) SiLU(z)
 //
-// One block of 256 threads per SM takes two heads of a group at a time, so that
-// G, B and C are formed and loaded once for both, every product has 128 rows,
-// and the state update's accumulator [2 x 64 head rows][N] fills all TMEM lanes:
+// A block takes two heads of a group at a time, so that G, B and C are formed
+// and loaded once for both, every product has 128 rows, and the state update's
+// accumulator [2 x 64 head rows][N] fills all TMEM lanes:
 //   G   C (K-major)     x B (K-major)         128 x 128, K = N
 //   Yc  C (K-major)     x H copy (K-major)    128 x 128, K = N
 //   Ym  M_h (in TMEM)   x X_h (MN-major)      128 x 64 per head, K = 128
 //   S   Xw^T (MN-major) x B (MN-major)        128 x N, K = 128, three times
 // TMEM: G, then Ym | Yc | M_0, M_1 (16-bit, two per column) | S: all 512 columns.
+//
+// One block of 640 threads per SM, its warps in roles that meet in mbarriers:
+// 0-7 form M and y (a warpgroup per head, a thread per token), 8-11 hold the
+// state (a thread per row), 12-15 form Xw a quarter of the chunk at a time, and
+// one warp each issues the products of y and of the state, issues the copies,
+// and forms the decays and finds the block's next piece of work.  The state's
+// products of a chunk run beside its y, and the state copy for the next chunk
+// is written while the state is updated, so the chain from chunk to chunk is
+// Xw -> S -> H -> copy -> Yc.
 //
 // Roundings to 16 bits: M and the H copy, once each (the operands of y, which
 // is itself rounded to 16 bits).  The state is not: Xw, a product of an fp32
@@ -47,7 +56,22 @@
 // alone from zero, then adds the published state of the block before, decayed,
 // publishes the sum and runs its range in full.  Blocks take their number from
 // a counter, so a block only ever waits for one that has started; the wait is
-// bounded all the same.
+// bounded all the same, as every wait here is: one that runs out sets a bit of
+// the fault word and the block drains its copies and products and leaves.
+//
+// What bounds it: the matrix instructions it needs (26 MFLOP per chunk and
+// pair at N = 128, half of them for the exact state) are 75 us at the rate of a
+// large bf16 product for 4 x 4096 tokens x 80 heads, its bytes 57 us; measured
+// 166 us on B200 (0.78 PFLOP/s, 2.2 TB/s), 224 us for one sequence of 32768
+// tokens x 24 heads, 235 us for 8192 tokens of ragged prompts x 80 heads with
+// their states, 17 us for one prompt of 37 tokens.  The rest is the chain
+// above, and the issue slots of Xw: its warps work 7 of a chunk's 9 thousand
+// cycles.  What made the difference on the way, at the 4 x 4096 x 80 size: one
+// group of 8 warps that does everything in turn 338 us; copies and products in
+// warps of their own 242; the state's warps apart from y's 234; two operand
+// buffers for S and the copy written on the way 212; rolled loops and short
+// waits, which keep the hot code of all roles (30 KB) inside the instruction
+// cache, 179; the gate compiled apart and accumulators given back early 166.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -68,10 +92,9 @@ namespace {
 
 constexpr int kP = 64;         // head dimension
 constexpr int kQ = 128;        // chunk length
-// Warps: 0-7 form M and y (a warpgroup per head), 8-11 hold the state, 12-15
-// form Xw, then one for the products of y, one for those of the state, one for
-// the copies, and one that forms the decays and finds the block's next run.  The registers of a block, 96 per thread at launch, are split
-// unevenly: the state's warps hold a whole state row each.
+// Warps: 0-7 the y group, 8-11 the state's, 12-15 Xw's, then the helpers.  The
+// registers of a block, 96 per thread at launch, are split unevenly: a thread
+// of the state's warps holds a whole state row.
 constexpr int kGroupY = 256, kGroupS = 128;  // threads of the y group, of the state's and Xw's
 constexpr int kMmaY = 16, kMmaS = 17, kTmaWarp = 18, kPlanWarp = 19;
 constexpr int kThreads = 640;
@@ -172,9 +195,9 @@ struct Lay {
   static constexpr int kH = kW + 2 * 24576;           // 128 rows x N 16-bit
   static constexpr int kArr = kH + kTile;             // two of Arrays
   static constexpr int kMax = kArr + 2 * 3104;        // unsigned [2]: largest |x| Delta of the chunk (fp16)
-  static constexpr int kUn = kMax + 16;               // float [2][2]: 1 / the power of two of Xw (fp16), by chunk and head
+  static constexpr int kUn = kMax + 16;               // float [2][2]: 1 / Xw's power of two (fp16), by chunk and head
   static constexpr int kBars = kUn + 16;              // mbarriers
-  static constexpr int kSlot = kBars + 192;  // TMEM base address  // TMEM base address
+  static constexpr int kSlot = kBars + 192;           // TMEM base address
   static constexpr int kBytes = kSlot + 16;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -280,6 +303,7 @@ struct Run {
 struct Runs {
   Cut A, E;
   int stage, useq, upair, npairs, per, ppg;
+  int seen, slot;  // the last sequence asked for and its slot: a sequence has a unit per pair
   bool same;
 
   __device__ __forceinline__ void start(const SsdPrefillParams& p, const Cut* cuts, int npairs_) {
@@ -288,6 +312,7 @@ struct Runs {
     npairs = npairs_;
     per = p.nheads / p.ngroups;
     ppg = (per + 1) / 2;  // heads and pairs per group
+    seen = -1;
     same = A.seq == E.seq && A.pair == E.pair;
     stage = same && A.chunk > 0 && E.chunk > 0 ? 0 : E.chunk > 0 ? 2 : 3;
     if (A.seq >= p.seq.nseq) stage = 6;
@@ -301,7 +326,7 @@ struct Runs {
   __device__ __forceinline__ void next(const SsdPrefillParams& p, Run* out) {
     Run run;
     run.n = -1;
-    int stage = this->stage, useq = this->useq, upair = this->upair;
+    int stage = this->stage, useq = this->useq, upair = this->upair, seen = this->seen, slot = this->slot;
     __syncwarp();
     while (stage < 6) {
       int pair, c1 = -1;
@@ -333,7 +358,9 @@ struct Runs {
       }
       run.slot = -1;
       if (p.state) {
-        run.slot = claim_slot_warp(p.slots, run.seq, &g_fault_prefill);
+        if (run.seq != seen) slot = claim_slot_warp(p.slots, run.seq, &g_fault_prefill);
+        seen = run.seq;
+        run.slot = slot;
         if (run.slot < 0) {
           if (stage == 1) stage = 6;  // the middle of a skipped sequence
           continue;
@@ -353,6 +380,8 @@ struct Runs {
       this->stage = stage;
       this->useq = useq;
       this->upair = upair;
+      this->seen = seen;
+      this->slot = slot;
     }
     __syncwarp();
   }
@@ -391,10 +420,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
 #pragma unroll
-    for (int i = 0; i < kNumBars; ++i) tc::mbar_init(bar(i), i < kBarW ? 1 : i == kBarM || i >= kBarY ? 8 : 4);
+    for (int i = 0; i < kNumBars; ++i)  // one arrival of the thread in charge, or one per warp of the group
+      tc::mbar_init(bar(i), i < kBarW ? 1 : i == kBarM || i >= kBarY ? 8 : 4);
     tc::fence_mbar_init();
   }
-  if (tid == 32 * kTmaWarp) {
+  if (tid == 32 * kTmaWarp && p.seq.tokens > 0) {
     tc::prefetch_map(&map_x);
     tc::prefetch_map(&map_b);
     tc::prefetch_map(&map_c);
@@ -501,8 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
               const float4 pv = pr[u], dv = dl[u];
-              const f2_t m01 = mul2(mul2(pk2(gv[4 * u], gv[4 * u + 1]), ex2_2(fma2(pk2(pv.x, pv.y), minus, pre2))), pk2(dv.x, dv.y));
-              const f2_t m23 = mul2(mul2(pk2(gv[4 * u + 2], gv[4 * u + 3]), ex2_2(fma2(pk2(pv.z, pv.w), minus, pre2))), pk2(dv.z, dv.w));
+              const f2_t e01 = ex2_2(fma2(pk2(pv.x, pv.y), minus, pre2));
+              const f2_t e23 = ex2_2(fma2(pk2(pv.z, pv.w), minus, pre2));
+              const f2_t m01 = mul2(mul2(pk2(gv[4 * u], gv[4 * u + 1]), e01), pk2(dv.x, dv.y));
+              const f2_t m23 = mul2(mul2(pk2(gv[4 * u + 2], gv[4 * u + 3]), e23), pk2(dv.z, dv.w));
               float m[4] = {lo2(m01), hi2(m01), lo2(m23), hi2(m23)};
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -539,7 +571,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
           float yc[16], ym[16];
-          tc::ld32x32b_x16_pair(tmem + lane_base + kYc + 64 * hd + 16 * i, tmem + lane_base + kG + 64 * hd + 16 * i, yc, ym);
+          const uint32_t col = tmem + lane_base + 64 * hd + 16 * i;
+          tc::ld32x32b_x16_pair(col + kYc, col + kG, yc, ym);
           if (i == 3) signal(kBarT);  // the next chunk's products may start
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -551,7 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int v = 0; v < 4; ++v) {
               const float2 f = Pk<T>::unpack(in[v]);
               const int at8 = 8 * u + 2 * v;
-              const f2_t r = fma2(D2, pk2(f.x, f.y), fma2(e2, pk2(yc[at8], yc[at8 + 1]), pk2(ym[at8], ym[at8 + 1])));
+              const f2_t r =
+                  fma2(D2, pk2(f.x, f.y), fma2(e2, pk2(yc[at8], yc[at8 + 1]), pk2(ym[at8], ym[at8 + 1])));
               o[2 * v] = lo2(r);
               o[2 * v + 1] = hi2(r);
             }
@@ -574,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = tid; i < nval * 8 * nh2; i += kGroupY) {
             const int hh = i / (nval * 8), r = (i >> 3) - hh * nval, cc = i & 7;
             const uint4 v = *reinterpret_cast<const uint4*>(sm + L::kX + (k & 1) * 32768 + hh * 16384 + swz(r, cc));
-            *reinterpret_cast<uint4*>(static_cast<T*>(p.y) + ((int64_t)(t0 + r) * p.nheads + h0 + hh) * kP + 8 * cc) = v;
+            T* const to = static_cast<T*>(p.y) + ((int64_t)(t0 + r) * p.nheads + h0 + hh) * kP;
+            *reinterpret_cast<uint4*>(to + 8 * cc) = v;
           }
         }
       }
@@ -626,7 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (nh2 == 1)  // the missing head's x is zero
 #pragma unroll 1
           for (int i = stid; i < 2048; i += kGroupS)
-            *reinterpret_cast<uint4*>(sm + L::kX + (i >> 10) * 32768 + 16384 + 16 * (i & 1023)) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(sm + L::kX + (i >> 10) * 32768 + 16384 + 16 * (i & 1023)) =
+                make_uint4(0, 0, 0, 0);
         signal(kBarH + (it & 1));
       }
       float psum = 0.f;  // log2 decay of the run so far (head hrow)
@@ -696,7 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsX));
     // ----------------------------------------------------------------- Xw
-    const int stid = tid - kGroupY - kGroupS, xh = blk >> 1, xc = 4 * (blk & 1);  // 32 columns of head xh, lanes over tokens
+    // a warp: 32 columns of head xh, lanes over tokens
+    const int stid = tid - kGroupY - kGroupS, xh = blk >> 1, xc = 4 * (blk & 1);
     for (uint32_t r = 0; next(r); ++r) {
       const int n = run->n, end = run->end, nh2 = run->nh2;
 #pragma unroll 1
@@ -727,18 +764,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           sync_x();
 #pragma unroll 1
           for (int e = 0; e < 2; ++e) {
-          unsigned m = 0;
+            unsigned m = 0;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint4 v = *reinterpret_cast<const uint4*>(xs + e * 16384 + swz(row, q));
-            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-          }
-          m = max(m & 0xffffu, m >> 16);
-          float top = __half2float(__ushort_as_half((unsigned short)m)) * fabsf(a.dl[e][row]);
-          top = top < 3.0e38f ? top : 1.f;
+            for (int q = 0; q < 8; ++q) {
+              const uint4 v = *reinterpret_cast<const uint4*>(xs + e * 16384 + swz(row, q));
+              const unsigned m0 = __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu);
+              m = __vmaxu2(m, __vmaxu2(m0, __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+            }
+            m = max(m & 0xffffu, m >> 16);
+            float top = __half2float(__ushort_as_half((unsigned short)m)) * fabsf(a.dl[e][row]);
+            top = top < 3.0e38f ? top : 1.f;
 #pragma unroll
-          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (lane == 0) atomicMax(sMax + e, __float_as_uint(top));
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (lane == 0) atomicMax(sMax + e, __float_as_uint(top));
           }
           sync_x();
           auto power = [](unsigned v) {  // 2^(14 - exponent of v), within fp32's range
@@ -789,200 +827,204 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsHelp));
-  if (warp == kTmaWarp) {
-    for (uint32_t r = 0; next(r); ++r) {
-      const int n = run->n, c0 = run->c0, end = run->end, h0 = run->h0, nh2 = run->nh2;
-      const bool full = run->full;
-      // ------------------------------------------------------------ copies
-      if (lane == 0 && n > 0) {
-        auto load = [&](int i, uint32_t off, const CUtensorMap* map, int col, int c, int nb) {
-          tc::expect_tx(bar(i), 16384u * nb);
+    if (warp == kTmaWarp) {
+      for (uint32_t r = 0; next(r); ++r) {
+        const int n = run->n, c0 = run->c0, end = run->end, h0 = run->h0, nh2 = run->nh2;
+        const bool full = run->full;
+        // ------------------------------------------------------------ copies
+        if (lane == 0 && n > 0) {
+          auto load = [&](int i, uint32_t off, const CUtensorMap* map, int col, int c, int nb) {
+            tc::expect_tx(bar(i), 16384u * nb);
 #pragma unroll 1
-          for (int b = 0; b < nb; ++b) tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, run->begin + c * kQ, bar(i));
-          arm(i);
-        };
-        auto load_b = [&](int c) { load(kBarB, L::kB, &map_b, run->g * N, c, N / 64); };
-        auto load_c = [&](int c) { load(kBarC, L::kC, &map_c, run->g * N, c, N / 64); };
-        auto load_x = [&](int c, uint32_t k) { load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, c, nh2); };
-        auto store_y = [&](int c, uint32_t k) {
+            for (int b = 0; b < nb; ++b)
+              tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, run->begin + c * kQ, bar(i));
+            arm(i);
+          };
+          auto load_b = [&](int c) { load(kBarB, L::kB, &map_b, run->g * N, c, N / 64); };
+          auto load_c = [&](int c) { load(kBarC, L::kC, &map_c, run->g * N, c, N / 64); };
+          auto load_x = [&](int c, uint32_t k) {
+            load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, c, nh2);
+          };
+          auto store_y = [&](int c, uint32_t k) {
 #pragma unroll 1
-          for (int b = 0; b < nh2; ++b)
-            tc::tma_store_2d(&map_y, (h0 + b) * kP, run->begin + c * kQ, sb + L::kX + (k & 1) * 32768 + 16384u * b);
-          tc::bulk_commit();
-        };
+            for (int b = 0; b < nh2; ++b)
+              tc::tma_store_2d(&map_y, (h0 + b) * kP, run->begin + c * kQ, sb + L::kX + (k & 1) * 32768 + 16384u * b);
+            tc::bulk_commit();
+          };
 #pragma unroll 1
-        for (int j = -1; j + 1 < n && ok; ++j) {  // chunk j + 1, each buffer as its last reader is done
-          const int c = c0 + j;
-          const uint32_t k = it + j, kf = itf + j;
-          if (j > 0 && full) {
-            wait2(kBarY, kf - 1);
-            if (!ok) break;
-            store_y(c - 1, k - 1);
-            tc::bulk_wait_read_all();
-          }
-          load_x(c + 1, k + 1);
-          if (j >= 0 && full) wait(kBarYc, kf);
-          if (ok && full) load_c(c + 1);
-          if (j >= 0) wait2(kBarSall, k);
-          if (ok) load_b(c + 1);
-        }
-        for (int j = max(0, n - 2); j < n && full; ++j) {  // the last two chunks' y; a ragged one is written by the y group
-          wait2(kBarY, itf + j);
-          if (ok && run->t0(j + 1) <= end) store_y(c0 + j, it + j);
-        }
-        tc::bulk_wait_read_all();
-      }
-      __syncwarp();
-      if (!done()) break;
-    }
-  } else if (warp == kMmaY) {
-    // Products.  The issuing lane is picked by elect.sync: in a branch on the
-    // thread number the compiler cannot take descriptors for uniform, and a
-    // product of 128 x 128 x 16 takes 170-220 cycles to issue instead of the
-    // 66 it takes to execute.
-    // ----------------------------------------------------- products of y
-    const uint64_t dc = tc::desc_sw128(sb + L::kC, 16, 1024), db0 = tc::desc_sw128(sb + L::kB, 16, 1024),
-                   dh = tc::desc_sw128(sb + L::kH, 16, 1024), dx0 = tc::desc_sw128(sb + L::kX, 16384, 1024);
-    for (uint32_t r = 0; next(r); ++r) {
-      const int n = run->full ? run->n : 0;
-#pragma unroll 1
-      for (int j = 0; j < n && ok; ++j) {
-        const uint32_t k = it + j, kf = itf + j;
-        wait(kBarB, k);
-        wait(kBarC, kf);
-        if (j > 0) wait(kBarT, kf - 1);  // the accumulators are read
-#pragma unroll 1
-        for (int e = 0; e < 2; ++e) {  // G = C B^T, then Yc = C H^T
-          if (e == 1) wait2(kBarH, k);
-          if (!ok) break;
-          tc::fence_after();
-          if (tc::elect()) {
-            const uint64_t db = e ? dh : db0;
-            const uint32_t to = tmem + kG + (kYc - kG) * e;
-#pragma unroll 1
-            for (int kk = 0; kk < N / 16; ++kk) {
-              const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-              tc::mma(to, dc + ko, db + ko, kId, kk > 0);
+          for (int j = -1; j + 1 < n && ok; ++j) {  // chunk j + 1, each buffer as its last reader is done
+            const int c = c0 + j;
+            const uint32_t k = it + j, kf = itf + j;
+            if (j > 0 && full) {
+              wait2(kBarY, kf - 1);
+              if (!ok) break;
+              store_y(c - 1, k - 1);
+              tc::bulk_wait_read_all();
             }
-            tc::commit(bar(kBarG + e));
+            load_x(c + 1, k + 1);
+            if (j >= 0 && full) wait(kBarYc, kf);
+            if (ok && full) load_c(c + 1);
+            if (j >= 0) wait2(kBarSall, k);
+            if (ok) load_b(c + 1);
           }
-          __syncwarp();
-          arm(kBarG + e);
-        }
-        wait2(kBarX, k);
-        wait(kBarM, kf);
-        if (run->t0(j + 1) > run->end) wait2(kBarR, k);  // a ragged chunk's x is cleared behind its end
-        if (!ok) break;
-        tc::fence_after();
-        if (tc::elect()) {
-          const uint64_t dx = dx0 + (k & 1) * (32768 >> 4);
-#pragma unroll 1
-          for (int i = 0; i < 16; ++i)  // two heads, 8 steps of 16 tokens; the second head's x is 16 KB on
-            tc::mma_ta(tmem + kG + 64 * (i >> 3), tmem + kM + 8 * i, dx + i * (2048 >> 4), kIdYm, (i & 7) != 0);
-          tc::commit(bar(kBarYm));
+          for (int j = max(0, n - 2); j < n && full; ++j) {  // the last two chunks' y (a ragged one: the y group)
+            wait2(kBarY, itf + j);
+            if (ok && run->t0(j + 1) <= end) store_y(c0 + j, it + j);
+          }
+          tc::bulk_wait_read_all();
         }
         __syncwarp();
-        arm(kBarYm);
+        if (!done()) break;
       }
-      if (!done()) break;
-    }
-  } else if (warp == kMmaS) {
-    // --------------------------------------------- products of the state
-    const uint64_t db = tc::desc_sw128(sb + L::kB, 16384, 1024), dw0 = tc::desc_sw128(sb + L::kW, 4096, 1024);
-    for (uint32_t r = 0; next(r); ++r) {
-      const int n = run->n;
+    } else if (warp == kMmaY) {
+      // Products.  The issuing lane is picked by elect.sync: in a branch on the
+      // thread number the compiler cannot take descriptors for uniform, and a
+      // product of 128 x 128 x 16 takes 170-220 cycles to issue instead of the
+      // 66 it takes to execute.
+      // ----------------------------------------------------- products of y
+      const uint64_t dc = tc::desc_sw128(sb + L::kC, 16, 1024), db0 = tc::desc_sw128(sb + L::kB, 16, 1024),
+                     dh = tc::desc_sw128(sb + L::kH, 16, 1024), dx0 = tc::desc_sw128(sb + L::kX, 16384, 1024);
+      for (uint32_t r = 0; next(r); ++r) {
+        const int n = run->full ? run->n : 0;
 #pragma unroll 1
-      for (int j = 0; j < n && ok; ++j) {
-        const uint32_t k = it + j;
-        wait(kBarB, k);
-        wait2(kBarH, k);
+        for (int j = 0; j < n && ok; ++j) {
+          const uint32_t k = it + j, kf = itf + j;
+          wait(kBarB, k);
+          wait(kBarC, kf);
+          if (j > 0) wait(kBarT, kf - 1);  // the accumulators are read
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          wait(kBarW + (q & 1), q >> 1);
+          for (int e = 0; e < 2; ++e) {  // G = C B^T, then Yc = C H^T
+            if (e == 1) wait2(kBarH, k);
+            if (!ok) break;
+            tc::fence_after();
+            if (tc::elect()) {
+              const uint64_t db = e ? dh : db0;
+              const uint32_t to = tmem + kG + (kYc - kG) * e;
+#pragma unroll 1
+              for (int kk = 0; kk < N / 16; ++kk) {
+                const uint32_t ko = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+                tc::mma(to, dc + ko, db + ko, kId, kk > 0);
+              }
+              tc::commit(bar(kBarG + e));
+            }
+            __syncwarp();
+            arm(kBarG + e);
+          }
+          wait2(kBarX, k);
+          wait(kBarM, kf);
+          if (run->t0(j + 1) > run->end) wait2(kBarR, k);  // a ragged chunk's x is cleared behind its end
           if (!ok) break;
           tc::fence_after();
           if (tc::elect()) {
-            const uint64_t dw = dw0 + (q & 1) * (24576 >> 4), dbq = db + q * (4096 >> 4);
+            const uint64_t dx = dx0 + (k & 1) * (32768 >> 4);
 #pragma unroll 1
-            for (int i = 0; i < 6; ++i)  // three pieces, two steps of 16 tokens
-              tc::mma(tmem + kS, dw + ((i >> 1) * 8192 + (i & 1) * 2048) / 16, dbq + (i & 1) * (2048 >> 4), kIdS,
-                      (q | i) != 0);
-            tc::commit(bar(kBarS + (q & 1)));
-            if (q == 3) tc::commit(bar(kBarSall + (k & 1)));
+            for (int i = 0; i < 16; ++i)  // two heads, 8 steps of 16 tokens; the second head's x is 16 KB on
+              tc::mma_ta(tmem + kG + 64 * (i >> 3), tmem + kM + 8 * i, dx + i * (2048 >> 4), kIdYm, (i & 7) != 0);
+            tc::commit(bar(kBarYm));
           }
           __syncwarp();
-          arm(kBarS + (q & 1));
+          arm(kBarYm);
         }
-        if (!ok) break;
-        arm(kBarSall + (k & 1));
+        if (!done()) break;
       }
-      if (!done()) break;
-    }
-  } else {
-    // ------------------- Delta and the decays of both heads; the next run
-    for (uint32_t r = 0; next(r); ++r) {
-      const int n = run->n, nh2 = run->nh2;
-      // lane: tokens 4 lane .. + 3 of the chunk, so a block of 32 is 8 lanes
-      const int seg = lane & 7;
+    } else if (warp == kMmaS) {
+      // --------------------------------------------- products of the state
+      const uint64_t db = tc::desc_sw128(sb + L::kB, 16384, 1024), dw0 = tc::desc_sw128(sb + L::kW, 4096, 1024);
+      for (uint32_t r = 0; next(r); ++r) {
+        const int n = run->n;
 #pragma unroll 1
-      for (int j = 0; j <= n; ++j) {
-        if (j == (n > 0)) {  // behind the first chunk's decays
-          Run* const then = &s_run[(r + 1) & 1];
-          s_runs.next(p, then);
-          if (lane == 0 && then->n > 0) {  // bring what its first chunk waits for into L2
-            tc::tma_prefetch_2d(&map_x, then->h0 * kP, then->t0(0));
-            if (then->nh2 > 1) tc::tma_prefetch_2d(&map_x, then->h0 * kP + kP, then->t0(0));
-            if (then->from_slot && p.state && !(p.slots.fresh && p.slots.fresh[then->seq]))
-              tc::bulk_prefetch(p.state + ((size_t)then->slot * p.nheads + then->h0) * kP * N, then->nh2 * kP * N * 4);
-          }
-        }
-        if (j == n) break;
-        const uint32_t k = it + j;
-        Arrays& a = arr[k & 1];
-        const int t = run->t0(j) + 4 * lane, left = run->end - t;
+        for (int j = 0; j < n && ok; ++j) {
+          const uint32_t k = it + j;
+          wait(kBarB, k);
+          wait2(kBarH, k);
 #pragma unroll 1
-        for (int e = 0; e < 2; ++e) {
-          const int h = run->h0 + min(e, nh2 - 1);
-          const T* const dtg = static_cast<const T*>(p.dt) + h;
-          T raw[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) raw[i] = dtg[(int64_t)min(t + i, run->end - 1) * p.lddt];
-          if (e == 0) {  // the readers of this buffer, two chunks before
-            if (j > 1) wait2(kBarH, k - 1);
-            if (j > 1 && run->full) wait2(kBarY, itf + j - 2);
+          for (int q = 0; q < 4; ++q) {
+            wait(kBarW + (q & 1), q >> 1);
+            if (!ok) break;
+            tc::fence_after();
+            if (tc::elect()) {
+              const uint64_t dw = dw0 + (q & 1) * (24576 >> 4), dbq = db + q * (4096 >> 4);
+#pragma unroll 1
+              for (int i = 0; i < 6; ++i)  // three pieces, two steps of 16 tokens
+                tc::mma(tmem + kS, dw + ((i >> 1) * 8192 + (i & 1) * 2048) / 16, dbq + (i & 1) * (2048 >> 4), kIdS,
+                        (q | i) != 0);
+              tc::commit(bar(kBarS + (q & 1)));
+              if (q == 3) tc::commit(bar(kBarSall + (k & 1)));
+            }
+            __syncwarp();
+            arm(kBarS + (q & 1));
           }
-          const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-          float d[4], in[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v = Elt<T>::to_f(raw[i]) + bias;
-            d[i] = p.softplus ? softplus_f(v) : v;
-            if (i >= left || e >= nh2) d[i] = 0.f;
-            in[i] = fmaf(d[i], A2, i ? in[i - 1] : 0.f);
-          }
-          float before = in[3], after = in[3];
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) {
-            const float u = __shfl_up_sync(0xffffffffu, before, o), v = __shfl_down_sync(0xffffffffu, after, o);
-            if (seg >= o) before += u;
-            if (seg + o < 8) after += v;
-          }
-          if (seg == 7) a.tot[e][lane >> 3] = before;
-          float u = __shfl_up_sync(0xffffffffu, before, 1), v = __shfl_down_sync(0xffffffffu, after, 1);
-          if (seg == 0) u = 0.f;
-          if (seg == 7) v = 0.f;
-          const float s2 = d[3] * A2, s1 = fmaf(d[2], A2, s2), s0 = fmaf(d[1], A2, s1);
-          *reinterpret_cast<float4*>(a.pre[e] + 4 * lane) = make_float4(u + in[0], u + in[1], u + in[2], u + in[3]);
-          *reinterpret_cast<float4*>(a.dl[e] + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
-          *reinterpret_cast<float4*>(a.f[e] + 4 * lane) =
-              make_float4(ex2(v + s0) * d[0], ex2(v + s1) * d[1], ex2(v + s2) * d[2], ex2(v) * d[3]);
+          if (!ok) break;
+          arm(kBarSall + (k & 1));
         }
-        __syncwarp();
-        if (lane == 0) arrive(bar(kBarA + (k & 1)));
+        if (!done()) break;
       }
-      if (!done()) break;
+    } else {
+      // ------------------- Delta and the decays of both heads; the next run
+      for (uint32_t r = 0; next(r); ++r) {
+        const int n = run->n, nh2 = run->nh2;
+        // lane: tokens 4 lane .. + 3 of the chunk, so a block of 32 is 8 lanes
+        const int seg = lane & 7;
+#pragma unroll 1
+        for (int j = 0; j <= n; ++j) {
+          if (j == (n > 0)) {  // behind the first chunk's decays
+            Run* const then = &s_run[(r + 1) & 1];
+            s_runs.next(p, then);
+            if (lane == 0 && then->n > 0) {  // bring what its first chunk waits for into L2
+              tc::tma_prefetch_2d(&map_x, then->h0 * kP, then->t0(0));
+              if (then->nh2 > 1) tc::tma_prefetch_2d(&map_x, then->h0 * kP + kP, then->t0(0));
+              if (then->from_slot && p.state && !(p.slots.fresh && p.slots.fresh[then->seq]))
+                tc::bulk_prefetch(p.state + ((size_t)then->slot * p.nheads + then->h0) * kP * N,
+                                  then->nh2 * kP * N * 4);
+            }
+          }
+          if (j == n) break;
+          const uint32_t k = it + j;
+          Arrays& a = arr[k & 1];
+          const int t = run->t0(j) + 4 * lane, left = run->end - t;
+#pragma unroll 1
+          for (int e = 0; e < 2; ++e) {
+            const int h = run->h0 + min(e, nh2 - 1);
+            const T* const dtg = static_cast<const T*>(p.dt) + h;
+            T raw[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[i] = dtg[(int64_t)min(t + i, run->end - 1) * p.lddt];
+            if (e == 0) {  // the readers of this buffer, two chunks before
+              if (j > 1) wait2(kBarH, k - 1);
+              if (j > 1 && run->full) wait2(kBarY, itf + j - 2);
+            }
+            const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+            float d[4], in[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float v = Elt<T>::to_f(raw[i]) + bias;
+              d[i] = p.softplus ? softplus_f(v) : v;
+              if (i >= left || e >= nh2) d[i] = 0.f;
+              in[i] = fmaf(d[i], A2, i ? in[i - 1] : 0.f);
+            }
+            float before = in[3], after = in[3];
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+              const float u = __shfl_up_sync(0xffffffffu, before, o), v = __shfl_down_sync(0xffffffffu, after, o);
+              if (seg >= o) before += u;
+              if (seg + o < 8) after += v;
+            }
+            if (seg == 7) a.tot[e][lane >> 3] = before;
+            float u = __shfl_up_sync(0xffffffffu, before, 1), v = __shfl_down_sync(0xffffffffu, after, 1);
+            if (seg == 0) u = 0.f;
+            if (seg == 7) v = 0.f;
+            const float s2 = d[3] * A2, s1 = fmaf(d[2], A2, s2), s0 = fmaf(d[1], A2, s1);
+            *reinterpret_cast<float4*>(a.pre[e] + 4 * lane) = make_float4(u + in[0], u + in[1], u + in[2], u + in[3]);
+            *reinterpret_cast<float4*>(a.dl[e] + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
+            *reinterpret_cast<float4*>(a.f[e] + 4 * lane) =
+                make_float4(ex2(v + s0) * d[0], ex2(v + s1) * d[1], ex2(v + s2) * d[2], ex2(v) * d[3]);
+          }
+          __syncwarp();
+          if (lane == 0) arrive(bar(kBarA + (k & 1)));
+        }
+        if (!done()) break;
+      }
     }
-  }
   }
 
   // Drain: copies and products in flight must be done before shared memory and

