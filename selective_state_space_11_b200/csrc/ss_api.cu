@@ -849,6 +849,7 @@ ss_status check_conv_tm(const char* fn, int64_t dim, int64_t width, int dtype, i
 void conv_tm_strips(int64_t tokens, int* strip, int* nstrip) {
   int64_t len = (tokens + 255) / 256;
   if (len < 32) len = 32;
+  len = (len + 3) / 4 * 4;  // whole groups of the kernel's tokens
   *strip = (int)len;
   *nstrip = (int)((tokens + len - 1) / len);
 }

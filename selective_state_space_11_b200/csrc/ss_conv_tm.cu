@@ -109,33 +109,49 @@ __device__ __forceinline__ void store_v(T* p, const float (&f)[V]) {
 // A thread's own rows on their way from global to shared memory: D rows of one
 // V-element vector per thread, copied asynchronously (cp.async) by the thread
 // that reads them, so that no barrier is needed and loads in flight cost no
-// registers.  Single elements (V == 1) are loaded when they are read.
-template <typename T, int V, int D>
+// registers.  Rows go in groups of kG.  Single elements (V == 1) are loaded
+// when they are read.
+constexpr int kG = 4;
+template <typename T, int V>
 struct Ring {
   static constexpr int kBytes = V * (int)sizeof(T);
+  static constexpr int D = 32 / (int)sizeof(T);  // 16 rows of 16-bit types, 8 of fp32
+  static constexpr int kPitch = 128 * kBytes;    // from row to row; a block has at most 128 threads
+  static constexpr int kSize = V > 1 ? D * kPitch : 0;
   unsigned char* slot;  // this thread's, in row 0
-  uint32_t pitch;       // bytes from row to row
-  __device__ __forceinline__ void start(unsigned char* base, int threads) {
-    slot = base + threadIdx.x * kBytes;
-    pitch = threads * kBytes;
-  }
-  __device__ __forceinline__ void put(int row, const T* p) const {
+  __device__ __forceinline__ void start(unsigned char* base) { slot = base + threadIdx.x * kBytes; }
+  // Row k of the group that starts at row g (a multiple of kG).
+  __device__ __forceinline__ unsigned char* at(int g, int k) const { return slot + (g & (D - 1)) * kPitch + k * kPitch; }
+  __device__ __forceinline__ void put(int g, int k, const T* p) const {
     if constexpr (V > 1) {
-      const unsigned to = static_cast<unsigned>(__cvta_generic_to_shared(slot + (row & (D - 1)) * pitch));
+      const unsigned to = static_cast<unsigned>(__cvta_generic_to_shared(at(g, k)));
       if constexpr (kBytes == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(to), "l"(p) : "memory");
       else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to), "l"(p) : "memory");
     }
   }
-  __device__ __forceinline__ void get(int row, const T* p, Raw<T, V>& r) const {
+  // The group at row g: rows p, p + ld, ..., the first n of them.
+  __device__ __forceinline__ void put_group(int g, const T* p, int64_t ld, int n) const {
+    if constexpr (V > 1) {
+      if (n >= kG) {
+#pragma unroll
+        for (int k = 0; k < kG; ++k, p += ld) put(g, k, p);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kG - 1; ++k, p += ld)
+          if (k < n) put(g, k, p);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int g, int k, const T* p, Raw<T, V>& r) const {
     if constexpr (V == 1) {
       r.load(p);
     } else if constexpr (kBytes == 16) {
-      const uint4 v = *reinterpret_cast<const uint4*>(slot + (row & (D - 1)) * pitch);
+      const uint4 v = *reinterpret_cast<const uint4*>(at(g, k));
       r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
     } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(slot + (row & (D - 1)) * pitch);
+      const uint2 v = *reinterpret_cast<const uint2*>(at(g, k));
       r.w[0] = v.x; r.w[1] = v.y;
     }
   }
@@ -198,8 +214,6 @@ __device__ __forceinline__ PieceAt piece_at(const Pieces& y, int c) {
   return {i == 0 ? y.p[0] : i == 1 ? y.p[1] : y.p[2], i == 0 ? y.width[0] : i == 1 ? y.width[1] : y.width[2], c};
 }
 
-constexpr int kRing = 8;  // rows in flight per thread
-
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(128) conv_tm_fwd_kernel(const ConvTmParams p, int tile) {
   if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, &g_fault_conv_tm);
@@ -218,11 +232,11 @@ __global__ void __launch_bounds__(128) conv_tm_fwd_kernel(const ConvTmParams p, 
   const T* __restrict__ x = static_cast<const T*>(p.x) + c;
   const int e = min(rt.end, s + tile);
   extern __shared__ __align__(16) unsigned char smem[];
-  Ring<T, V, kRing> ring;
-  ring.start(smem, blockDim.x);
+  Ring<T, V> ring;
+  ring.start(smem);
 #pragma unroll
-  for (int u = 0; u < kRing - 1; ++u) {
-    if (s + u < e) ring.put(u, x + (int64_t)(s + u) * p.ldx);
+  for (int g = 0; g < ring.D - kG; g += kG) {
+    ring.put_group(g, x + (int64_t)(s + g) * p.ldx, p.ldx, e - s - g);
     cp_async_commit();
   }
   constexpr int NP = pairs<V>();
@@ -274,26 +288,41 @@ __global__ void __launch_bounds__(128) conv_tm_fwd_kernel(const ConvTmParams p, 
   }
   const PieceAt at = piece_at(p.y, c);
   T* __restrict__ y = static_cast<T*>(at.p) + at.col;
-#pragma unroll 4
-  for (int t = s; t < e; ++t) {
-    if (t + kRing - 1 < e) ring.put(t - s + kRing - 1, x + (int64_t)(t + kRing - 1) * p.ldx);
+  const int64_t ldx = p.ldx, ldy = at.width;
+#pragma unroll 1
+  for (int t = s; t < e; t += kG) {
+    const int ahead = t + ring.D - kG;
+    ring.put_group(ahead - s, x + (int64_t)ahead * ldx, ldx, e - ahead);
     cp_async_commit();
-    cp_async_wait_group<kRing - 1>();
-    Raw<T, V> r;
-    ring.get(t - s, x + (int64_t)t * p.ldx, r);
-    f2_t o[NP];
+    cp_async_wait_group<ring.D / kG - 1>();
+    const T* xt = x + (int64_t)t * ldx;
+    T* yt = y + (int64_t)t * ldy;
+    auto group = [&](auto whole) {
+      Raw<T, V> r[kG];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const f2_t xv = pair_at(r, i);
-      o[i] = fma2(wk[W - 1][i], xv, bv[i]);
+      for (int k = 0; k < kG; ++k, xt += ldx) {
+        r[k].zero();
+        if (decltype(whole)::value || t + k < e) ring.get(t - s, k, xt, r[k]);
+      }
 #pragma unroll
-      for (int k = 0; k < W - 1; ++k) o[i] = fma2(wk[k][i], win[k][i], o[i]);
-      if (p.silu) o[i] = silu_2(o[i]);
+      for (int k = 0; k < kG; ++k, yt += ldy) {
+        f2_t o[NP];
 #pragma unroll
-      for (int k = 0; k + 1 < W - 1; ++k) win[k][i] = win[k + 1][i];
-      if (W > 1) win[H - 1][i] = xv;
-    }
-    store_pairs<T, V>(y + (int64_t)t * at.width, o);
+        for (int i = 0; i < NP; ++i) {
+          const f2_t xv = pair_at(r[k], i);
+          o[i] = fma2(wk[W - 1][i], xv, bv[i]);
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j) o[i] = fma2(wk[j][i], win[j][i], o[i]);
+          if (p.silu) o[i] = silu_2(o[i]);
+#pragma unroll
+          for (int j = 0; j + 1 < W - 1; ++j) win[j][i] = win[j + 1][i];
+          if (W > 1) win[H - 1][i] = xv;
+        }
+        if (decltype(whole)::value || t + k < e) store_pairs<T, V>(yt, o);
+      }
+    };
+    if (t + kG <= e) group(std::true_type{});
+    else group(std::false_type{});
   }
 }
 
@@ -337,26 +366,28 @@ __global__ void __launch_bounds__(128) conv_tm_bwd_kernel(const ConvTmParams p) 
   T* __restrict__ dx = static_cast<T*>(p.dx) + c;
   const int last = min(p.seq.tokens, e + W - 1);  // tokens whose dpre the strip needs
   extern __shared__ __align__(16) unsigned char smem[];
-  Ring<T, V, kRing> ringx, ringg;
-  ringx.start(smem, blockDim.x);
-  ringg.start(smem + kRing * blockDim.x * V * sizeof(T), blockDim.x);
+  const int64_t ldx = p.ldx, ldg = at.width, lddx = p.lddx;
+  Ring<T, V> ringx, ringg;
+  ringx.start(smem);
+  ringg.start(smem + ringx.kSize);
 #pragma unroll
-  for (int u = 0; u < kRing - 1; ++u) {
-    if (s + u < last) {
-      ringx.put(u, x + (int64_t)(s + u) * p.ldx);
-      ringg.put(u, dy + (int64_t)(s + u) * at.width);
-    }
+  for (int g = 0; g < ringx.D - kG; g += kG) {
+    ringx.put_group(g, x + (int64_t)(s + g) * ldx, ldx, last - s - g);
+    ringg.put_group(g, dy + (int64_t)(s + g) * ldg, ldg, last - s - g);
     cp_async_commit();
   }
   constexpr int NP = pairs<V>();
-  f2_t wk[W][NP], bv[NP], win[H][NP], dp[W][NP], dwk[W][NP], dbv[NP];
+  // win, dp: the inputs and dpre of the W-1 tokens before the one that comes next
+  f2_t wk[W][NP], bv[NP], win[H][NP], dp[H][NP], dwk[W][NP], dbv[NP];
   load_taps<V, W>(p, c, wk, bv);
-  int ps[W];  // positions of tokens t-(W-1) .. t, or -1
+  int ps[W];  // positions of the last W tokens in their sequences, or -1
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     dbv[i] = pk2(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < W; ++k) dwk[k][i] = dp[k][i] = pk2(0.f, 0.f);
+    for (int k = 0; k < W; ++k) dwk[k][i] = pk2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < H; ++k) dp[k][i] = pk2(0.f, 0.f);
   }
 #pragma unroll
   for (int k = 0; k < W; ++k) ps[k] = -1;
@@ -371,77 +402,136 @@ __global__ void __launch_bounds__(128) conv_tm_bwd_kernel(const ConvTmParams p) 
   }
   Walk walk;
   walk.start(p.seq, s);
-#pragma unroll 4
-  for (int tt = s; tt < e + W - 1; ++tt) {
-    const int n = tt + kRing - 1;
-    if (n < last) {
-      ringx.put(n - s, x + (int64_t)n * p.ldx);
-      ringg.put(n - s, dy + (int64_t)n * at.width);
-    }
+  const f2_t zero = pk2(0.f, 0.f), one = pk2(1.f, 1.f);
+  // dL/dpre of a token from its dL/dy
+  auto dpre = [&](f2_t pre, f2_t g) {
+    if (!SILU) return g;
+    const f2_t den = add2(one, ex2_2(mul2(pre, pk2(-kLog2e, -kLog2e))));
+    const f2_t sg = pk2(rcp(lo2(den)), rcp(hi2(den)));
+    return mul2(g, mul2(sg, fma2(pre, fma2(sg, pk2(-1.f, -1.f), one), one)));
+  };
+#pragma unroll 1
+  for (int tt = s; tt < e + W - 1; tt += kG) {
+    const int ahead = tt + ringx.D - kG;
+    ringx.put_group(ahead - s, x + (int64_t)ahead * ldx, ldx, last - ahead);
+    ringg.put_group(ahead - s, dy + (int64_t)ahead * ldg, ldg, last - ahead);
     cp_async_commit();
-    cp_async_wait_group<kRing - 1>();
-    const bool there = tt < last;
-    Raw<T, V> rx, rg;
-    rx.zero();
-    rg.zero();
-    if (there) {
-      ringx.get(tt - s, x + (int64_t)tt * p.ldx, rx);
-      ringg.get(tt - s, dy + (int64_t)tt * at.width, rg);
-    }
-    const int pos = there ? walk.pos(p.seq, tt) : -1;
+    cp_async_wait_group<ringx.D / kG - 1>();
+    const T* xt = x + (int64_t)tt * ldx;
+    const T* gt = dy + (int64_t)tt * ldg;
+    T* dxt = dx + (int64_t)(tt - (W - 1)) * lddx;
+    const int pos0 = tt < last ? walk.pos(p.seq, tt) : -1;
+    // A group of the strip's own tokens, or the W-1 behind it, all in one sequence from its W-th token on: all
+    // taps of each, and all tokens that dx of the tokens W-1 before takes, are of that sequence.  Nothing to mask.
+    auto group = [&](auto own) {
+      constexpr bool kOwn = decltype(own)::value;
+      constexpr int kN = kOwn ? kG : W - 1;
+      Raw<T, V> rx[kN], rg[kN];
 #pragma unroll
-    for (int k = 0; k + 1 < W; ++k) ps[k] = ps[k + 1];
-    ps[W - 1] = pos;
-    const bool own = tt < e;  // else only dx of earlier tokens needs this dpre
-    // From its W-th token on, all taps of a token, and all tokens that dx of
-    // token tt-(W-1) takes, are of the token's own sequence: nothing to mask.
-    const f2_t zero = pk2(0.f, 0.f), one = pk2(1.f, 1.f);
-    f2_t dxv[NP];
-    auto token = [&](auto plain) {
-      constexpr bool kPlain = decltype(plain)::value;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      f2_t tap[W];
-#pragma unroll
-      for (int k = 0; k < W - 1; ++k) tap[k] = win[k][i];
-      tap[W - 1] = pair_at(rx, i);
-      if (!kPlain)
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-          if (pos < W - 1 - k) tap[k] = zero;
-      f2_t pre = bv[i];
-#pragma unroll
-      for (int k = 0; k < W; ++k) pre = fma2(wk[k][i], tap[k], pre);
-      f2_t d = pair_at(rg, i);
-      if (SILU) {
-        const f2_t den = add2(one, ex2_2(mul2(pre, pk2(-kLog2e, -kLog2e))));
-        const f2_t sg = pk2(rcp(lo2(den)), rcp(hi2(den)));
-        d = mul2(d, mul2(sg, fma2(pre, fma2(sg, pk2(-1.f, -1.f), one), one)));
+      for (int k = 0; k < kN; ++k, xt += ldx, gt += ldg) {
+        ringx.get(tt - s, k, xt, rx[k]);
+        ringg.get(tt - s, k, gt, rg[k]);
       }
-      if (!kPlain && pos < 0) d = zero;  // a token of no sequence
-      if (kPlain || (own && pos >= 0)) {
-        dbv[i] = add2(dbv[i], d);
+      f2_t dxv[kN][NP];
 #pragma unroll
-        for (int k = 0; k < W; ++k) dwk[k][i] = fma2(d, tap[k], dwk[k][i]);
+      for (int i = 0; i < NP; ++i) {
+        f2_t in[W - 1 + kN], d[W - 1 + kN];
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+          in[k] = win[k][i];
+          d[k] = dp[k][i];
+        }
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+          in[W - 1 + k] = pair_at(rx[k], i);
+          f2_t pre = bv[i];
+#pragma unroll
+          for (int j = 0; j < W; ++j) pre = fma2(wk[j][i], in[k + j], pre);
+          const f2_t dv = dpre(pre, pair_at(rg[k], i));
+          d[W - 1 + k] = dv;
+          if (kOwn) {
+            dbv[i] = add2(dbv[i], dv);
+#pragma unroll
+            for (int j = 0; j < W; ++j) dwk[j][i] = fma2(dv, in[k + j], dwk[j][i]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+          f2_t a = zero;
+#pragma unroll
+          for (int m = 0; m < W; ++m) a = fma2(wk[W - 1 - m][i], d[k + m], a);
+          dxv[k][i] = a;
+        }
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+          win[k][i] = in[kN + k];
+          dp[k][i] = d[kN + k];
+        }
       }
 #pragma unroll
-      for (int k = 0; k + 1 < W; ++k) dp[k][i] = dp[k + 1][i];
-      dp[W - 1][i] = d;
-      // dx of token tt-(W-1): the dpre of the m-th token after it, where that is of the same sequence
-      f2_t a = zero;
+      for (int k = 0; k < kN; ++k, dxt += lddx)
+        if (k >= W - 1 || tt > s) store_pairs<T, V>(dxt, dxv[k]);  // (dx before the strip is another's)
 #pragma unroll
-      for (int m = 0; m < W; ++m)
-        if (kPlain || (ps[0] >= 0 && ps[m] >= m)) a = fma2(wk[W - 1 - m][i], dp[m][i], a);
-      dxv[i] = a;
-#pragma unroll
-      for (int k = 0; k + 1 < W - 1; ++k) win[k][i] = win[k + 1][i];
-      if (W > 1) win[H - 1][i] = pair_at(rx, i);
-    }
+      for (int k = 0; k < W; ++k) ps[k] = pos0 + kN - W + k;
     };
-    if (own && pos >= W - 1) token(std::true_type{});
-    else token(std::false_type{});
-    const int td = tt - (W - 1);
-    if (td >= s) store_pairs<T, V>(dx + (int64_t)td * p.lddx, dxv);
+    if (pos0 >= W - 1 && tt + kG <= min(e, walk.end)) {
+      group(std::true_type{});
+      continue;
+    }
+    if constexpr (W > 1 && W - 1 <= kG) {
+      if (pos0 >= W - 1 && tt == e && tt + W - 1 <= walk.end) {
+        group(std::false_type{});
+        break;
+      }
+    }
+#pragma unroll 1
+    for (int k = 0; k < kG && tt + k < e + W - 1; ++k, xt += ldx, gt += ldg, dxt += lddx) {
+      const int t = tt + k;
+      Raw<T, V> rx, rg;
+      rx.zero();
+      rg.zero();
+      if (t < last) {
+        ringx.get(tt - s, k, xt, rx);
+        ringg.get(tt - s, k, gt, rg);
+      }
+      const int pos = t < last ? walk.pos(p.seq, t) : -1;
+#pragma unroll
+      for (int j = 0; j + 1 < W; ++j) ps[j] = ps[j + 1];
+      ps[W - 1] = pos;
+      f2_t dxv[NP];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        f2_t in[W], d[W];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+          in[j] = pos < W - 1 - j ? zero : win[j][i];
+          d[j] = dp[j][i];
+        }
+        in[W - 1] = pair_at(rx, i);
+        f2_t pre = bv[i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) pre = fma2(wk[j][i], in[j], pre);
+        const f2_t dv = pos < 0 ? zero : dpre(pre, pair_at(rg, i));  // (a token of no sequence)
+        d[W - 1] = dv;
+        if (t < e && pos >= 0) {  // else only dx of earlier tokens needs this dpre
+          dbv[i] = add2(dbv[i], dv);
+#pragma unroll
+          for (int j = 0; j < W; ++j) dwk[j][i] = fma2(dv, in[j], dwk[j][i]);
+        }
+        // dx of token t-(W-1): the dpre of the m-th token after it, where that is of the same sequence
+        f2_t a = zero;
+#pragma unroll
+        for (int m = 0; m < W; ++m)
+          if (ps[0] >= 0 && ps[m] >= m) a = fma2(wk[W - 1 - m][i], d[m], a);
+        dxv[i] = a;
+#pragma unroll
+        for (int j = 0; j + 1 < W - 1; ++j) win[j][i] = win[j + 1][i];
+        if (W > 1) win[H - 1][i] = in[W - 1];
+#pragma unroll
+        for (int j = 0; j + 1 < W; ++j) dp[j][i] = d[j + 1];
+      }
+      if (t - (W - 1) >= s) store_pairs<T, V>(dxt, dxv);
+    }
   }
   float* part = p.part + ((size_t)blockIdx.x * p.dim + c) * (W + 1);
 #pragma unroll
@@ -497,11 +587,11 @@ cudaError_t run(const ConvTmParams& p, bool backward, int sms, cudaStream_t s) {
     int tile = 32;
     while (tile > 8 && (long long)(p.seq.tokens / tile) * ny * nt < (long long)sms * 1024) tile /= 2;
     const long long tiles = ragged_tiles(p.seq, tile);
-    conv_tm_fwd_kernel<T, V, W><<<dim3((unsigned)tiles, ny), nt, V > 1 ? kRing * nt * V * sizeof(T) : 0, s>>>(p, tile);
+    conv_tm_fwd_kernel<T, V, W><<<dim3((unsigned)tiles, ny), nt, Ring<T, V>::kSize, s>>>(p, tile);
     return cudaGetLastError();
   }
   if (p.nstrip > 0) {
-    const size_t smem = V > 1 ? 2 * kRing * nt * V * sizeof(T) : 0;
+    const size_t smem = 2 * Ring<T, V>::kSize;
     if (p.silu) conv_tm_bwd_kernel<T, V, W, true><<<dim3((unsigned)p.nstrip, ny), nt, smem, s>>>(p);
     else conv_tm_bwd_kernel<T, V, W, false><<<dim3((unsigned)p.nstrip, ny), nt, smem, s>>>(p);
     const cudaError_t e = cudaGetLastError();
