@@ -197,7 +197,7 @@ struct Lay {
   static constexpr int kMax = kArr + 2 * 3104;        // unsigned [2]: largest |x| Delta of the chunk (fp16)
   static constexpr int kUn = kMax + 16;               // float [2][2]: 1 / Xw's power of two (fp16), by chunk and head
   static constexpr int kBars = kUn + 16;              // mbarriers
-  static constexpr int kSlot = kBars + 192;           // TMEM base address
+  static constexpr int kSlot = kBars + 256;           // TMEM base address
   static constexpr int kBytes = kSlot + 16;
   static constexpr int kAlloc = kBytes + 1024;
 };
@@ -229,11 +229,21 @@ enum : int {
   kBarW = 13,     // [2] a quarter of Xw is written
   kBarM = 15,     // M is written
   kBarR = 16,     // [2] Xw's warps are done with x
-  kBarH = 18,     // [2] the state copy is written and S is read: the next chunk's products may start
+  kBarH = 18,     // [2] the state copy is written
   kBarY = 20,     // [2] y is in place of x
   kBarT = 22,     // y's accumulators are read
-  kNumBars = 23
+  kBarE = 23,     // S is read: the next chunk's products may start
+  kBarN = 24,     // [kRuns] a run is found
+  kBarD = 28,     // [kRuns] a run is done in the warps of all roles but the planning one
+  kNumBars = 32
 };
+constexpr int kRuns = 4;  // runs known at a time
+__host__ __device__ constexpr unsigned arrivals(int i) {
+  return i < kBarW || (i >= kBarN && i < kBarD) ? 1  // the thread in charge
+         : i >= kBarD                          ? 19  // all warps but the planning one
+         : i == kBarM || (i >= kBarY && i <= kBarT) ? 8  // the warps of the y group
+                                               : 4;  // those of the state's or Xw's
+}
 
 __device__ __forceinline__ uint32_t swz(int r, int c) {
   return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
@@ -241,19 +251,22 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-// Barriers of the y group, of Xw's warps and of the state's; the last is true
-// everywhere if any thread's flag is set.
-__device__ __forceinline__ void sync_y() { asm volatile("barrier.cta.sync 1, 256;\n" ::: "memory"); }
-__device__ __forceinline__ void sync_x() { asm volatile("barrier.cta.sync 2, 128;\n" ::: "memory"); }
-__device__ __forceinline__ bool sync_s(bool v) {
+// Barriers of the y group, of Xw's warps and of the state's; true everywhere
+// if any thread's flag is set.
+template <int ID, int THREADS>
+__device__ __forceinline__ bool sync_or(bool v) {
   int r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, 3, 128, p;\n selp.b32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n"
+      " selp.b32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"((int)v)
+      : "r"((int)v), "n"(ID), "n"(THREADS)
       : "memory");
   return r != 0;
 }
+__device__ __forceinline__ bool sync_y(bool v) { return sync_or<1, kGroupY>(v); }
+__device__ __forceinline__ bool sync_x(bool v) { return sync_or<2, kGroupS>(v); }
+__device__ __forceinline__ bool sync_s(bool v) { return sync_or<3, kGroupS>(v); }
 // 32 bytes of one thread, 32-byte aligned.
 __device__ __forceinline__ void ld_v8(const float* p, float* v) {
   asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
@@ -394,6 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap map_y) {
   using L = Lay<N>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr int kPieces = kBf16 ? 3 : 2;
   constexpr uint32_t kId = tc::idesc_f16(kBf16, 128, 128, false, false);  // G, Yc
   constexpr uint32_t kIdS = tc::idesc_f16(kBf16, 128, N, true, true);
   constexpr uint32_t kIdYm = tc::idesc_f16(kBf16, 128, 64, false, true);
@@ -408,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* const sUn = reinterpret_cast<float*>(sm + L::kUn);
   uint32_t* const sslot = reinterpret_cast<uint32_t*>(sm + L::kSlot);
   __shared__ unsigned s_block;
-  __shared__ Run s_run[2];
+  __shared__ Run s_run[kRuns];
   __shared__ Runs s_runs;
   auto bar = [&](int i) { return sb + L::kBars + 8u * static_cast<uint32_t>(i); };
 
@@ -419,9 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int hrow = row >> 6;         // the head of state row `row`
 
   if (tid == 0) {
-#pragma unroll
-    for (int i = 0; i < kNumBars; ++i)  // one arrival of the thread in charge, or one per warp of the group
-      tc::mbar_init(bar(i), i < kBarW ? 1 : i == kBarM || i >= kBarY ? 8 : 4);
+#pragma unroll 1
+    for (int i = 0; i < kNumBars; ++i) tc::mbar_init(bar(i), arrivals(i));
     tc::fence_mbar_init();
   }
   if (tid == 32 * kTmaWarp && p.seq.tokens > 0) {
@@ -452,8 +465,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     b = __shfl_sync(0xffffffffu, b, 0);
     if (lane == 0) s_block = b;
     if (lane == 0) s_runs.start(p, reinterpret_cast<const Cut*>(ws + play.cuts) + b, npairs);
-    __syncwarp();
-    s_runs.next(p, s_run);
   }
   __syncthreads();
   const int me = (int)s_block;
@@ -484,23 +495,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   uint32_t it = 0, itf = 0;  // chunks, and chunks in full, so far
 
-  // Run r of the block: found by the planning warp while the run before is
-  // under way; false behind the last.
+  // Run r of the block, found by the planning warp ahead of time; false behind
+  // the last, or when a wait of the role has run out (`any`: of any of its threads).
   const Run* run = nullptr;
-  auto next = [&](uint32_t r) -> bool {
-    run = &s_run[r & 1];
-    return run->n >= 0;
+  auto next = [&](uint32_t r, auto any) -> bool {
+    wait(kBarN + (int)(r % kRuns), r / kRuns);
+    run = &s_run[r % kRuns];
+    return !any(!ok) && run->n >= 0;
   };
-  // The run is done in all warps; false when the block gives up.
-  auto done = [&]() -> bool {
+  auto any_warp = [&](bool v) { return __any_sync(0xffffffffu, v) != 0; };
+  // The run is done in this warp.  The roles flow from run to run, each as far
+  // as its barriers let it; only behind a run of the state alone they meet, so
+  // that the roles which have no part in it find the barriers in phase.
+  auto done = [&](uint32_t r) {
     const int n = run->n;
+    const bool full = run->full;
     it += n;
-    if (run->full) itf += n;
-    return !__syncthreads_or(!ok);
+    if (full) itf += n;
+    __syncwarp();
+    if (lane == 0 && warp != kPlanWarp) arrive(bar(kBarD + (int)(r % kRuns)));
+    if (!full) wait(kBarD + (int)(r % kRuns), r / kRuns);
   };
 
   if (warp < 8) {
-    for (uint32_t r = 0; next(r); ++r) {
+    for (uint32_t r = 0; next(r, sync_y); ++r) {
       const int n = run->n, end = run->end, h0 = run->h0, nh2 = run->nh2;
       const bool full = run->full;
       // ----------------------------------------------------------- M and y
@@ -601,9 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (mine) *at = pack8<T>(o);
           }
         }
-        signal(kBarY + (kf & 1));
         if (nval < kQ) {  // the rows of a ragged chunk, one by one
-          sync_y();
+          sync_y(false);
 #pragma unroll 1
           for (int i = tid; i < nval * 8 * nh2; i += kGroupY) {
             const int hh = i / (nval * 8), r = (i >> 3) - hh * nval, cc = i & 7;
@@ -612,12 +629,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4*>(to + 8 * cc) = v;
           }
         }
+        signal(kBarY + (kf & 1));
       }
-      if (!done()) break;
+      done(r);
     }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsS));
-    for (uint32_t r = 0; next(r); ++r) {
+    for (uint32_t r = 0; next(r, sync_s); ++r) {
       const int n = run->n, h0 = run->h0, nh2 = run->nh2;
       const bool full = run->full;
       // ----------------------------------------------------- the state -------
@@ -658,11 +676,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (n > 0) {
         if (full) write_copy();
-        if (nh2 == 1)  // the missing head's x is zero
-#pragma unroll 1
-          for (int i = stid; i < 2048; i += kGroupS)
-            *reinterpret_cast<uint4*>(sm + L::kX + (i >> 10) * 32768 + 16384 + 16 * (i & 1023)) =
-                make_uint4(0, 0, 0, 0);
         signal(kBarH + (it & 1));
       }
       float psum = 0.f;  // log2 decay of the run so far (head hrow)
@@ -699,6 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = q / 8; i < q / 8 + 2; ++i)
               *reinterpret_cast<uint4*>(sm + L::kH + (i / 8) * 16384 + swz(row, i % 8)) = pack8<T>(hs + 8 * i);
         }
+        signal(kBarE);
         if (more) signal(kBarH + ((k + 1) & 1));
       }
       ok = !sync_s(!ok);
@@ -727,14 +741,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < N; i += 8) st_v8(st + i, hs + i);
       }
-      if (!done()) break;
+      done(r);
     }
   } else if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsX));
     // ----------------------------------------------------------------- Xw
     // a warp: 32 columns of head xh, lanes over tokens
     const int stid = tid - kGroupY - kGroupS, xh = blk >> 1, xc = 4 * (blk & 1);
-    for (uint32_t r = 0; next(r); ++r) {
+    for (uint32_t r = 0; next(r, sync_x); ++r) {
       const int n = run->n, end = run->end, nh2 = run->nh2;
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
@@ -743,25 +757,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Arrays& a = arr[k & 1];
         unsigned char* const xs = sm + L::kX + (k & 1) * 32768;
         wait2(kBarX, k);
-        if (nval < kQ) {  // rows behind the sequence belong to others: no NaN of theirs may meet a zero weight
-          wait(kBarB, k);
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-          for (int i = stid; i < (kQ - nval) * 8; i += kGroupS) {
-            const uint32_t o = (nval + i / 8) * 128 + (i & 7) * 16;
-#pragma unroll
-            for (int b = 0; b < N / 64; ++b) *reinterpret_cast<uint4*>(sm + L::kB + 16384 * b + o) = zero;
-            *reinterpret_cast<uint4*>(xs + o) = zero;
-            *reinterpret_cast<uint4*>(xs + 16384 + o) = zero;
-          }
-          sync_x();
-        }
         wait2(kBarA, k);
-        if (j == 0 && nh2 == 1) wait2(kBarH, k);  // the missing head's x is cleared
         float scale = 1.f;
         if constexpr (!kBf16) {  // fp16: the power of two that puts max (|x| Delta) below 2^15
           if (stid < 2) sMax[stid] = 0u;
-          sync_x();
+          sync_x(false);
 #pragma unroll 1
           for (int e = 0; e < 2; ++e) {
             unsigned m = 0;
@@ -774,11 +774,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = max(m & 0xffffu, m >> 16);
             float top = __half2float(__ushort_as_half((unsigned short)m)) * fabsf(a.dl[e][row]);
             top = top < 3.0e38f ? top : 1.f;
+            if (row >= nval || e >= nh2) top = 0.f;
 #pragma unroll
             for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             if (lane == 0) atomicMax(sMax + e, __float_as_uint(top));
           }
-          sync_x();
+          sync_x(false);
           auto power = [](unsigned v) {  // 2^(14 - exponent of v), within fp32's range
             const int e = (int)(v >> 23) - 127;
             return v == 0 ? 0 : min(100, max(-100, 14 - e));
@@ -786,20 +787,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           scale = __uint_as_float((unsigned)(127 + power(sMax[xh])) << 23);
           if (stid < 2) sUn[2 * (k & 1) + stid] = __uint_as_float((unsigned)(127 - power(sMax[stid])) << 23);
         }
-        // ---- Xw, 32 tokens at a time, as three 16-bit pieces
+        // ---- Xw, 32 tokens at a time, as 16-bit pieces.  Rows behind the
+        // sequence belong to others, and a missing head has none: no NaN of
+        // theirs may meet a zero weight, so x, and with its last rows B, become zero there.
+        const int xval = xh < nh2 ? nval : 0;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           float later = 0.f;  // log2 decay of the blocks behind
           for (int b = q + 1; b < 4; ++b) later += a.tot[xh][b];
           const float w = a.f[xh][32 * q + lane] * ex2(later) * scale;
           const f2_t w2 = pk2(w, w), minus = pk2(-1.f, -1.f);
-          const unsigned char* const from = xs + xh * 16384;
+          unsigned char* const from = xs + xh * 16384;
+          const bool live = 32 * q + lane < xval;
           unsigned char* const to = sm + L::kW + (q & 1) * 24576 + xh * 4096;
           // the products of the quarter before the last have read the buffer
-          if (q > 1 || j > 0) wait(kBarS + (q & 1), q > 1 ? 0 : 1);
+          if (q > 1 || k > 0) wait(kBarS + (q & 1), q > 1 ? 0 : 1);
 #pragma unroll 2
           for (int k4 = xc; k4 < xc + 4; ++k4) {
-            const uint4 xv = *reinterpret_cast<const uint4*>(from + swz(32 * q + lane, k4));
+            uint4* const xp = reinterpret_cast<uint4*>(from + swz(32 * q + lane, k4));
+            if (!live) *xp = make_uint4(0, 0, 0, 0);
+            const uint4 xv = *xp;
             const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
             uint32_t u[4], v[4], z[4];
 #pragma unroll
@@ -810,71 +817,86 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 f0 = Pk<T>::unpack(u[e]);
               const f2_t x1 = fma2(pk2(f0.x, f0.y), minus, x0);
               v[e] = Pk<T>::pack(lo2(x1), hi2(x1));
-              const float2 f1 = Pk<T>::unpack(v[e]);
-              const f2_t x2 = fma2(pk2(f1.x, f1.y), minus, x1);
-              z[e] = Pk<T>::pack(lo2(x2), hi2(x2));
+              if (kPieces == 3) {
+                const float2 f1 = Pk<T>::unpack(v[e]);
+                const f2_t x2 = fma2(pk2(f1.x, f1.y), minus, x1);
+                z[e] = Pk<T>::pack(lo2(x2), hi2(x2));
+              }
             }
             const uint32_t o = swz(lane, k4);
             *reinterpret_cast<uint4*>(to + o) = make_uint4(u[0], u[1], u[2], u[3]);
             *reinterpret_cast<uint4*>(to + 8192 + o) = make_uint4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<uint4*>(to + 16384 + o) = make_uint4(z[0], z[1], z[2], z[3]);
+            if (kPieces == 3) *reinterpret_cast<uint4*>(to + 16384 + o) = make_uint4(z[0], z[1], z[2], z[3]);
+          }
+          if (32 * q + 32 > nval) {
+            wait(kBarB, k);
+            const int first = max(nval - 32 * q, 0);
+#pragma unroll 1
+            for (int i = 8 * first + stid; i < 256; i += kGroupS)
+#pragma unroll
+              for (int b = 0; b < N / 64; ++b)
+                *reinterpret_cast<uint4*>(sm + L::kB + 16384 * b + 4096 * q + 16 * i) = make_uint4(0, 0, 0, 0);
           }
           signal(kBarW + (q & 1));
         }
         if (lane == 0) arrive(bar(kBarR + (k & 1)));  // (the signal above ordered the warp's accesses)
       }
-      if (!done()) break;
+      done(r);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsHelp));
     if (warp == kTmaWarp) {
-      for (uint32_t r = 0; next(r); ++r) {
-        const int n = run->n, c0 = run->c0, end = run->end, h0 = run->h0, nh2 = run->nh2;
+      // y of the last two chunks in full, to be stored when its buffer is needed
+      // or at the end (t < 0: a ragged chunk, whose y the y group writes)
+      int t_a = -1, h_a = 0, t_b = -1, h_b = 0;  // h: first head, and the number of heads above bit 16
+      auto store_y = [&](int t, int h, uint32_t k) {
+        if (t < 0) return;
+#pragma unroll 1
+        for (int b = 0; b < h >> 16; ++b)
+          tc::tma_store_2d(&map_y, ((h & 0xffff) + b) * kP, t, sb + L::kX + (k & 1) * 32768 + 16384u * b);
+        tc::bulk_commit();
+      };
+      for (uint32_t r = 0; next(r, any_warp); ++r) {
+        const int n = run->n, end = run->end, h0 = run->h0, nh2 = run->nh2;
         const bool full = run->full;
         // ------------------------------------------------------------ copies
-        if (lane == 0 && n > 0) {
-          auto load = [&](int i, uint32_t off, const CUtensorMap* map, int col, int c, int nb) {
+        if (lane == 0) {
+          auto load = [&](int i, uint32_t off, const CUtensorMap* map, int col, int t, int nb) {
             tc::expect_tx(bar(i), 16384u * nb);
 #pragma unroll 1
-            for (int b = 0; b < nb; ++b)
-              tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, run->begin + c * kQ, bar(i));
+            for (int b = 0; b < nb; ++b) tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, t, bar(i));
             arm(i);
           };
-          auto load_b = [&](int c) { load(kBarB, L::kB, &map_b, run->g * N, c, N / 64); };
-          auto load_c = [&](int c) { load(kBarC, L::kC, &map_c, run->g * N, c, N / 64); };
-          auto load_x = [&](int c, uint32_t k) {
-            load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, c, nh2);
-          };
-          auto store_y = [&](int c, uint32_t k) {
 #pragma unroll 1
-            for (int b = 0; b < nh2; ++b)
-              tc::tma_store_2d(&map_y, (h0 + b) * kP, run->begin + c * kQ, sb + L::kX + (k & 1) * 32768 + 16384u * b);
-            tc::bulk_commit();
-          };
-#pragma unroll 1
-          for (int j = -1; j + 1 < n && ok; ++j) {  // chunk j + 1, each buffer as its last reader is done
-            const int c = c0 + j;
+          for (int j = 0; j < n && ok; ++j) {  // each buffer as its last reader is done
             const uint32_t k = it + j, kf = itf + j;
-            if (j > 0 && full) {
-              wait2(kBarY, kf - 1);
+            const int t = run->t0(j);
+            if (full) {
+              if (kf > 1) wait2(kBarY, kf - 2);
               if (!ok) break;
-              store_y(c - 1, k - 1);
+              store_y(t_a, h_a, k);
+              t_a = t_b;
+              h_a = h_b;
+              t_b = t + kQ <= end ? t : -1;
+              h_b = h0 | nh2 << 16;
               tc::bulk_wait_read_all();
             }
-            load_x(c + 1, k + 1);
-            if (j >= 0 && full) wait(kBarYc, kf);
-            if (ok && full) load_c(c + 1);
-            if (j >= 0) wait2(kBarSall, k);
-            if (ok) load_b(c + 1);
+            load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, t, nh2);
+            if (full) {
+              if (kf > 0) wait(kBarYc, kf - 1);
+              if (ok) load(kBarC, L::kC, &map_c, run->g * N, t, N / 64);
+            }
+            if (k > 0) wait2(kBarSall, k - 1);
+            if (ok) load(kBarB, L::kB, &map_b, run->g * N, t, N / 64);
           }
-          for (int j = max(0, n - 2); j < n && full; ++j) {  // the last two chunks' y (a ragged one: the y group)
-            wait2(kBarY, itf + j);
-            if (ok && run->t0(j + 1) <= end) store_y(c0 + j, it + j);
-          }
-          tc::bulk_wait_read_all();
         }
-        __syncwarp();
-        if (!done()) break;
+        done(r);
+      }
+      if (lane == 0) {
+        if (itf > 1) wait2(kBarY, itf - 2);
+        if (ok) store_y(t_a, h_a, it);
+        if (itf > 0) wait2(kBarY, itf - 1);
+        if (ok) store_y(t_b, h_b, it + 1);
       }
     } else if (warp == kMmaY) {
       // Products.  The issuing lane is picked by elect.sync: in a branch on the
@@ -884,14 +906,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------- products of y
       const uint64_t dc = tc::desc_sw128(sb + L::kC, 16, 1024), db0 = tc::desc_sw128(sb + L::kB, 16, 1024),
                      dh = tc::desc_sw128(sb + L::kH, 16, 1024), dx0 = tc::desc_sw128(sb + L::kX, 16384, 1024);
-      for (uint32_t r = 0; next(r); ++r) {
+      for (uint32_t r = 0; next(r, any_warp); ++r) {
         const int n = run->full ? run->n : 0;
 #pragma unroll 1
         for (int j = 0; j < n && ok; ++j) {
           const uint32_t k = it + j, kf = itf + j;
           wait(kBarB, k);
           wait(kBarC, kf);
-          if (j > 0) wait(kBarT, kf - 1);  // the accumulators are read
+          if (kf > 0) wait(kBarT, kf - 1);  // the accumulators are read
 #pragma unroll 1
           for (int e = 0; e < 2; ++e) {  // G = C B^T, then Yc = C H^T
             if (e == 1) wait2(kBarH, k);
@@ -925,18 +947,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           arm(kBarYm);
         }
-        if (!done()) break;
+        done(r);
       }
     } else if (warp == kMmaS) {
       // --------------------------------------------- products of the state
       const uint64_t db = tc::desc_sw128(sb + L::kB, 16384, 1024), dw0 = tc::desc_sw128(sb + L::kW, 4096, 1024);
-      for (uint32_t r = 0; next(r); ++r) {
+      for (uint32_t r = 0; next(r, any_warp); ++r) {
         const int n = run->n;
 #pragma unroll 1
         for (int j = 0; j < n && ok; ++j) {
           const uint32_t k = it + j;
           wait(kBarB, k);
-          wait2(kBarH, k);
+          if (k > 0) wait(kBarE, k - 1);
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             wait(kBarW + (q & 1), q >> 1);
@@ -945,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (tc::elect()) {
               const uint64_t dw = dw0 + (q & 1) * (24576 >> 4), dbq = db + q * (4096 >> 4);
 #pragma unroll 1
-              for (int i = 0; i < 6; ++i)  // three pieces, two steps of 16 tokens
+              for (int i = 0; i < 2 * kPieces; ++i)  // the pieces, two steps of 16 tokens
                 tc::mma(tmem + kS, dw + ((i >> 1) * 8192 + (i & 1) * 2048) / 16, dbq + (i & 1) * (2048 >> 4), kIdS,
                         (q | i) != 0);
               tc::commit(bar(kBarS + (q & 1)));
@@ -957,27 +979,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           arm(kBarSall + (k & 1));
         }
-        if (!done()) break;
+        done(r);
       }
     } else {
       // ------------------- Delta and the decays of both heads; the next run
-      for (uint32_t r = 0; next(r); ++r) {
+      auto publish = [&](uint32_t r) {  // run r
+        if (r >= kRuns) wait(kBarD + (int)(r % kRuns), r / kRuns - 1);
+        if (any_warp(!ok)) return;
+        Run* const then = &s_run[r % kRuns];
+        s_runs.next(p, then);
+        if (lane == 0) {
+          if (then->n > 0) {  // bring what its first chunk waits for into L2
+            tc::tma_prefetch_2d(&map_x, then->h0 * kP, then->t0(0));
+            if (then->nh2 > 1) tc::tma_prefetch_2d(&map_x, then->h0 * kP + kP, then->t0(0));
+            if (then->from_slot && p.state && !(p.slots.fresh && p.slots.fresh[then->seq]))
+              tc::bulk_prefetch(p.state + ((size_t)then->slot * p.nheads + then->h0) * kP * N,
+                                then->nh2 * kP * N * 4);
+          }
+          arrive(bar(kBarN + (int)(r % kRuns)));
+        }
+      };
+      publish(0);
+      for (uint32_t r = 0; next(r, any_warp); ++r) {
         const int n = run->n, nh2 = run->nh2;
         // lane: tokens 4 lane .. + 3 of the chunk, so a block of 32 is 8 lanes
         const int seg = lane & 7;
 #pragma unroll 1
         for (int j = 0; j <= n; ++j) {
-          if (j == (n > 0)) {  // behind the first chunk's decays
-            Run* const then = &s_run[(r + 1) & 1];
-            s_runs.next(p, then);
-            if (lane == 0 && then->n > 0) {  // bring what its first chunk waits for into L2
-              tc::tma_prefetch_2d(&map_x, then->h0 * kP, then->t0(0));
-              if (then->nh2 > 1) tc::tma_prefetch_2d(&map_x, then->h0 * kP + kP, then->t0(0));
-              if (then->from_slot && p.state && !(p.slots.fresh && p.slots.fresh[then->seq]))
-                tc::bulk_prefetch(p.state + ((size_t)then->slot * p.nheads + then->h0) * kP * N,
-                                  then->nh2 * kP * N * 4);
-            }
-          }
+          if (j == (n > 0)) publish(r + 1);  // behind the first chunk's decays
           if (j == n) break;
           const uint32_t k = it + j;
           Arrays& a = arr[k & 1];
@@ -990,8 +1019,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) raw[i] = dtg[(int64_t)min(t + i, run->end - 1) * p.lddt];
             if (e == 0) {  // the readers of this buffer, two chunks before
-              if (j > 1) wait2(kBarH, k - 1);
-              if (j > 1 && run->full) wait2(kBarY, itf + j - 2);
+              if (k > 1) wait2(kBarH, k - 1);
+              if (run->full && itf + j > 1) wait2(kBarY, itf + j - 2);
             }
             const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
             float d[4], in[4];
@@ -1022,7 +1051,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) arrive(bar(kBarA + (k & 1)));
         }
-        if (!done()) break;
+        done(r);
       }
     }
   }
