@@ -96,9 +96,9 @@ constexpr int kQ = 128;        // chunk length
 // registers of a block, 96 per thread at launch, are split unevenly: a thread
 // of the state's warps holds a whole state row.
 constexpr int kGroupY = 256, kGroupS = 128;  // threads of the y group, of the state's and Xw's
-constexpr int kMmaY = 16, kMmaS = 17, kTmaWarp = 18, kPlanWarp = 19;
+constexpr int kMmaY = 16, kMmaS = 17, kTmaWarp = 18;  // and 19, the decays
 constexpr int kThreads = 640;
-constexpr int kRegsS = 168, kRegsX = 72, kRegsHelp = 48;  // 2 x 96 + 168 + 72 + 48 = 5 x 96 per quarter of the SM
+constexpr int kRegsS = 168, kRegsX = 64, kRegsHelp = 56;  // 2 x 96 + 168 + 64 + 56 = 5 x 96 per quarter of the SM
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr uint32_t kFlagLimit = 1u << 22;  // polls of a predecessor's flag
 constexpr uint32_t kG = 0, kYc = 128, kM = 256, kS = 384;  // TMEM columns (Ym over G)
@@ -245,7 +245,7 @@ enum : int {
 constexpr int kRuns = 4;  // runs known at a time
 __host__ __device__ constexpr unsigned arrivals(int i) {
   return i < kBarW || (i >= kBarN && i < kBarD) ? 1  // the thread in charge
-         : i >= kBarD                          ? 19  // all warps but the planning one
+         : i >= kBarD                          ? kThreads / 32
          : i == kBarM || (i >= kBarY && i <= kBarT) ? 8  // the warps of the y group
                                                : 4;  // those of the state's or Xw's
 }
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PlanLayout play = plan_layout(p.seq.nseq, blocks, N);
   unsigned* const flags = reinterpret_cast<unsigned*>(ws + play.flags);
   float4* const carry = reinterpret_cast<float4*>(ws + play.carry);
-  if (warp == kPlanWarp) {
+  if (warp == kTmaWarp) {
     unsigned b = 0;
     if (lane == 0) b = atomicAdd(flags + blocks, 1u);
     b = __shfl_sync(0xffffffffu, b, 0);
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   uint32_t it = 0, itf = 0;  // chunks, and chunks in full, so far
 
-  // Run r of the block, found by the planning warp ahead of time; false behind
+  // Run r of the block, found by the copying warp ahead of time; false behind
   // the last, or when a wait of the role has run out (`any`: of any of its threads).
   const Run* run = nullptr;
   auto next = [&](uint32_t r, auto any) -> bool {
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     it += n;
     if (full) itf += n;
     __syncwarp();
-    if (lane == 0 && warp != kPlanWarp) arrive(bar(kBarD + (int)(r % kRuns)));
+    if (lane == 0) arrive(bar(kBarD + (int)(r % kRuns)));
     if (!full) wait(kBarD + (int)(r % kRuns), r / kRuns);
   };
 
@@ -860,32 +860,51 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tma_store_2d(&map_y, ((h & 0xffff) + b) * kP, t, sb + L::kX + (k & 1) * 32768 + 16384u * b);
         tc::bulk_commit();
       };
+      auto publish = [&](uint32_t r) {  // run r
+        if (r >= kRuns) wait(kBarD + (int)(r % kRuns), r / kRuns - 1);
+        if (any_warp(!ok)) return;
+        Run* const then = &s_run[r % kRuns];
+        s_runs.next(p, then);
+        if (lane == 0) {
+          arrive(bar(kBarN + (int)(r % kRuns)));
+          if (then->n > 0) {  // bring what its first chunk waits for into L2
+            tc::tma_prefetch_2d(&map_x, then->h0 * kP, then->t0(0));
+            if (then->nh2 > 1) tc::tma_prefetch_2d(&map_x, then->h0 * kP + kP, then->t0(0));
+            if (then->from_slot && p.state && !(p.slots.fresh && p.slots.fresh[then->seq]))
+              tc::bulk_prefetch(p.state + ((size_t)then->slot * p.nheads + then->h0) * kP * N,
+                                then->nh2 * kP * N * 4);
+          }
+        }
+        __syncwarp();
+      };
+      publish(0);
       for (uint32_t r = 0; next(r, any_warp); ++r) {
         const int n = run->n, end = run->end, h0 = run->h0, nh2 = run->nh2;
         const bool full = run->full;
-        // ------------------------------------------------------------ copies
-        if (lane == 0) {
-          auto load = [&](int i, uint32_t off, const CUtensorMap* map, int col, int t, int nb) {
-            tc::expect_tx(bar(i), 16384u * nb);
+        // ------------------------------------------------ copies; the next run
+        auto load = [&](int i, uint32_t off, const CUtensorMap* map, int col, int t, int nb) {
+          tc::expect_tx(bar(i), 16384u * nb);
 #pragma unroll 1
-            for (int b = 0; b < nb; ++b) tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, t, bar(i));
-            arm(i);
-          };
+          for (int b = 0; b < nb; ++b) tc::tma_load_2d(sb + off + 16384u * b, map, col + 64 * b, t, bar(i));
+          arm(i);
+        };
 #pragma unroll 1
-          for (int j = 0; j < n && ok; ++j) {  // each buffer as its last reader is done
-            const uint32_t k = it + j, kf = itf + j;
-            const int t = run->t0(j);
+        for (int j = 0; j <= n; ++j) {
+          if (j == (n > 0)) publish(r + 1);  // behind the first chunk's copies
+          if (j == n) break;
+          const uint32_t k = it + j, kf = itf + j;
+          const int t = run->t0(j);
+          if (lane == 0 && ok) {  // each buffer as its last reader is done
             if (full) {
               if (kf > 1) wait2(kBarY, kf - 2);
-              if (!ok) break;
-              store_y(t_a, h_a, k);
+              if (ok) store_y(t_a, h_a, k);
               t_a = t_b;
               h_a = h_b;
               t_b = t + kQ <= end ? t : -1;
               h_b = h0 | nh2 << 16;
               tc::bulk_wait_read_all();
             }
-            load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, t, nh2);
+            if (ok) load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, t, nh2);
             if (full) {
               if (kf > 0) wait(kBarYc, kf - 1);
               if (ok) load(kBarC, L::kC, &map_c, run->g * N, t, N / 64);
@@ -893,6 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (k > 0) wait2(kBarSall, k - 1);
             if (ok) load(kBarB, L::kB, &map_b, run->g * N, t, N / 64);
           }
+          __syncwarp();
         }
         done(r);
       }
@@ -986,73 +1006,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         done(r);
       }
     } else {
-      // ------------------- Delta and the decays of both heads; the next run
-      auto publish = [&](uint32_t r) {  // run r
-        if (r >= kRuns) wait(kBarD + (int)(r % kRuns), r / kRuns - 1);
-        if (any_warp(!ok)) return;
-        Run* const then = &s_run[r % kRuns];
-        s_runs.next(p, then);
-        if (lane == 0) {
-          arrive(bar(kBarN + (int)(r % kRuns)));
-          if (then->n > 0) {  // bring what its first chunk waits for into L2
-            tc::tma_prefetch_2d(&map_x, then->h0 * kP, then->t0(0));
-            if (then->nh2 > 1) tc::tma_prefetch_2d(&map_x, then->h0 * kP + kP, then->t0(0));
-            if (then->from_slot && p.state && !(p.slots.fresh && p.slots.fresh[then->seq]))
-              tc::bulk_prefetch(p.state + ((size_t)then->slot * p.nheads + then->h0) * kP * N,
-                                then->nh2 * kP * N * 4);
-          }
-        }
-        __syncwarp();
-      };
-      publish(0);
+      // ------------- Delta and the decays of both heads, as pairs (lo: the first)
+      // lane: tokens 4 lane .. + 3 of the chunk, so a block of 32 is 8 lanes
+      const int seg = lane & 7;
+      const f2_t zero = pk2(0.f, 0.f);
       for (uint32_t r = 0; next(r, any_warp); ++r) {
-        const int n = run->n, nh2 = run->nh2;
-        // lane: tokens 4 lane .. + 3 of the chunk, so a block of 32 is 8 lanes
-        const int seg = lane & 7;
+        const int n = run->n, h = run->h0, h1 = run->nh2 - 1;  // (a missing head's are computed and dropped)
+        const f2_t A2 = pk2(p.A[h] * kLog2e, p.A[h + h1] * kLog2e);
+        const f2_t bias = p.dt_bias ? pk2(p.dt_bias[h], p.dt_bias[h + h1]) : zero;
 #pragma unroll 1
-        for (int j = 0; j <= n; ++j) {
-          if (j == (n > 0)) publish(r + 1);  // behind the first chunk's decays
-          if (j == n) break;
+        for (int j = 0; j < n; ++j) {
           const uint32_t k = it + j;
           Arrays& a = arr[k & 1];
           const int t = run->t0(j) + 4 * lane, left = run->end - t;
-#pragma unroll 1
-          for (int e = 0; e < 2; ++e) {
-            const int h = run->h0 + min(e, nh2 - 1);
-            const T* const dtg = static_cast<const T*>(p.dt) + h;
-            T raw[4];
+          const T* const dtg = static_cast<const T*>(p.dt) + h;
+          f2_t d[4], in[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) raw[i] = dtg[(int64_t)min(t + i, run->end - 1) * p.lddt];
-            if (e == 0) {  // the readers of this buffer, two chunks before
-              if (k > 1) wait2(kBarH, k - 1);
-              if (run->full && itf + j > 1) wait2(kBarY, itf + j - 2);
-            }
-            const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-            float d[4], in[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float v = Elt<T>::to_f(raw[i]) + bias;
-              d[i] = p.softplus ? softplus_f(v) : v;
-              if (i >= left || e >= nh2) d[i] = 0.f;
-              in[i] = fmaf(d[i], A2, i ? in[i - 1] : 0.f);
-            }
-            float before = in[3], after = in[3];
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) {
-              const float u = __shfl_up_sync(0xffffffffu, before, o), v = __shfl_down_sync(0xffffffffu, after, o);
-              if (seg >= o) before += u;
-              if (seg + o < 8) after += v;
-            }
-            if (seg == 7) a.tot[e][lane >> 3] = before;
-            float u = __shfl_up_sync(0xffffffffu, before, 1), v = __shfl_down_sync(0xffffffffu, after, 1);
-            if (seg == 0) u = 0.f;
-            if (seg == 7) v = 0.f;
-            const float s2 = d[3] * A2, s1 = fmaf(d[2], A2, s2), s0 = fmaf(d[1], A2, s1);
-            *reinterpret_cast<float4*>(a.pre[e] + 4 * lane) = make_float4(u + in[0], u + in[1], u + in[2], u + in[3]);
-            *reinterpret_cast<float4*>(a.dl[e] + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
-            *reinterpret_cast<float4*>(a.f[e] + 4 * lane) =
-                make_float4(ex2(v + s0) * d[0], ex2(v + s1) * d[1], ex2(v + s2) * d[2], ex2(v) * d[3]);
+          for (int i = 0; i < 4; ++i) {
+            const T* const at = dtg + (int64_t)min(t + i, run->end - 1) * p.lddt;
+            d[i] = pk2(Elt<T>::to_f(at[0]), Elt<T>::to_f(at[h1]));
           }
+          // the readers of this buffer, two chunks before
+          if (k > 1) wait2(kBarH, k - 1);
+          if (run->full && itf + j > 1) wait2(kBarY, itf + j - 2);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            d[i] = add2(d[i], bias);
+            if (p.softplus) d[i] = pk2(softplus_f(lo2(d[i])), softplus_f(hi2(d[i])));
+            if (i >= left) d[i] = zero;
+            if (h1 == 0) d[i] = pk2(lo2(d[i]), 0.f);
+            in[i] = i ? fma2(d[i], A2, in[i - 1]) : mul2(d[i], A2);
+          }
+          f2_t before = in[3], after = in[3];
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) {
+            const f2_t u = __shfl_up_sync(0xffffffffu, before, o), v = __shfl_down_sync(0xffffffffu, after, o);
+            if (seg >= o) before = add2(before, u);
+            if (seg + o < 8) after = add2(after, v);
+          }
+          if (seg == 7) {
+            a.tot[0][lane >> 3] = lo2(before);
+            a.tot[1][lane >> 3] = hi2(before);
+          }
+          f2_t u = __shfl_up_sync(0xffffffffu, before, 1), v = __shfl_down_sync(0xffffffffu, after, 1);
+          if (seg == 0) u = zero;
+          if (seg == 7) v = zero;
+          f2_t f[4];  // from the token to the end of its block
+          f[3] = v;
+          f[2] = fma2(d[3], A2, zero);
+          f[1] = fma2(d[2], A2, f[2]);
+          f[0] = add2(fma2(d[1], A2, f[1]), v);
+          f[1] = add2(f[1], v);
+          f[2] = add2(f[2], v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            in[i] = add2(u, in[i]);
+            f[i] = mul2(ex2_2(f[i]), d[i]);
+          }
+          auto put = [&](float (&to)[2][kQ], const f2_t (&x)[4]) {
+            *reinterpret_cast<float4*>(to[0] + 4 * lane) = make_float4(lo2(x[0]), lo2(x[1]), lo2(x[2]), lo2(x[3]));
+            *reinterpret_cast<float4*>(to[1] + 4 * lane) = make_float4(hi2(x[0]), hi2(x[1]), hi2(x[2]), hi2(x[3]));
+          };
+          put(a.pre, in);
+          put(a.dl, d);
+          put(a.f, f);
           __syncwarp();
           if (lane == 0) arrive(bar(kBarA + (k & 1)));
         }
