@@ -9,12 +9,12 @@
 // into up to three contiguous arrays (x, B, C), which is what the scan takes.
 //
 // Both passes are bound by HBM: forward 2 + 2 bytes per element in bf16
-// against W FMAs and two SFU operations.  A thread owns V adjacent channels
-// (one 16-byte load a token) and walks a tile of tokens with the W-1 previous
-// inputs in registers and the next kRing - 1 rows on their way to its own
-// shared-memory slots: plain loads held the forward at 128 us for 16384 x 5376
-// bf16 (352 MB), these take 77 us (4.6 TB/s), where half of a warp's time is
-// still the products; one token's fp32 work goes two channels to an instruction.
+// against W FMAs and two SFU operations.  A thread owns 4 adjacent channels
+// and walks a tile of tokens, four at a time, with the W-1 previous inputs in
+// registers and the next rows on their way to its own shared-memory slots; two
+// channels go through an instruction as an fp32 pair.  At 16384 x 5376 bf16 (352
+// MB) the forward takes 69 us (5.1 TB/s): plain loads held it at 128, one token
+// at a time at 77.
 //
 // Forward: tiles never straddle two sequences (ss_ragged.cuh), so only a
 // sequence's first tile needs the incoming window, and the threads that read
@@ -25,10 +25,11 @@
 // the token axis whatever the sequences.  dx[t] needs dpre[t .. t+W-1], so a
 // strip recomputes dpre for W-1 tokens behind it.  dw and dbias stay in
 // registers over the strip, go to one partial per strip, and a second kernel
-// sums the strips in order: no atomics, bitwise reproducible.  191 us at the
-// same size (529 MB, 2.8 TB/s; 330 us before the ring and the pairs): W + 1
-// products and the SiLU' of every token are formed, then 2 W more for dx and
-// dw, some 40 instructions an element, which is what bounds it.
+// sums the strips in order: no atomics, bitwise reproducible.  139 us at the
+// same size (529 MB, 3.8 TB/s).  W + 1 products and the SiLU' of every token
+// are formed, then 2 W more for dw and dx, 30 instructions an element: the fp32
+// pipe and its latency bound it.  One token at a time, masked wherever it is, it
+// took 191 us and 45 instructions; 5 blocks per SM, in 96 registers, 170.
 #include <type_traits>
 
 #include "ss_device.cuh"
@@ -121,7 +122,9 @@ struct Ring {
   unsigned char* slot;  // this thread's, in row 0
   __device__ __forceinline__ void start(unsigned char* base) { slot = base + threadIdx.x * kBytes; }
   // Row k of the group that starts at row g (a multiple of kG).
-  __device__ __forceinline__ unsigned char* at(int g, int k) const { return slot + (g & (D - 1)) * kPitch + k * kPitch; }
+  __device__ __forceinline__ unsigned char* at(int g, int k) const {
+    return slot + (g & (D - 1)) * kPitch + k * kPitch;
+  }
   __device__ __forceinline__ void put(int g, int k, const T* p) const {
     if constexpr (V > 1) {
       const unsigned to = static_cast<unsigned>(__cvta_generic_to_shared(at(g, k)));
@@ -612,12 +615,12 @@ cudaError_t run_w(const ConvTmParams& p, bool backward, int sms, cudaStream_t s)
   return cudaErrorInvalidValue;
 }
 
-// Channels per thread: a 16-byte vector forward; backward, whose windows and
-// sums need W times the registers, an 8-byte one for 16-bit types.
+// Channels per thread: 4 where rows are aligned, whatever the type: the windows,
+// taps and sums of more would not fit the registers of the backward.
 template <typename T>
 cudaError_t run_t(const ConvTmParams& p, bool backward, bool vec, int sms, cudaStream_t s) {
   if (!vec) return run_w<T, 1>(p, backward, sms, s);
-  return backward ? run_w<T, 4>(p, true, sms, s) : run_w<T, 4>(p, false, sms, s);
+  return run_w<T, 4>(p, backward, sms, s);
 }
 
 cudaError_t dispatch(const ConvTmParams& p, bool backward, DType dt, bool vec, int sms, cudaStream_t s) {

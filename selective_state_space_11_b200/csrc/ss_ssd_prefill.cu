@@ -20,25 +20,26 @@
 //   G   C (K-major)     x B (K-major)         128 x 128, K = N
 //   Yc  C (K-major)     x H copy (K-major)    128 x 128, K = N
 //   Ym  M_h (in TMEM)   x X_h (MN-major)      128 x 64 per head, K = 128
-//   S   Xw^T (MN-major) x B (MN-major)        128 x N, K = 128, three times
+//   S   Xw^T (MN-major) x B (MN-major)        128 x N, K = 128, once per piece
 // TMEM: G, then Ym | Yc | M_0, M_1 (16-bit, two per column) | S: all 512 columns.
 //
-// One block of 640 threads per SM, its warps in roles that meet in mbarriers:
-// 0-7 form M and y (a warpgroup per head, a thread per token), 8-11 hold the
-// state (a thread per row), 12-15 form Xw a quarter of the chunk at a time, and
-// one warp each issues the products of y and of the state, issues the copies,
-// and forms the decays and finds the block's next piece of work.  The state's
-// products of a chunk run beside its y, and the state copy for the next chunk
-// is written while the state is updated, so the chain from chunk to chunk is
-// Xw -> S -> H -> copy -> Yc.
+// One block of 640 threads per SM, its warps in roles that meet in mbarriers
+// and flow from run to run of the block's work without meeting otherwise: 0-7
+// form M and y (a warpgroup per head, a thread per token), 8-11 hold the state
+// (a thread per row), 12-15 form Xw a quarter of the chunk at a time, and one
+// warp each issues the products of y, those of the state, issues the copies and
+// finds the next run, and forms the decays.  The state's products of a chunk run
+// beside its y, and the state copy for the next chunk is written while the state
+// is updated, so the chain from chunk to chunk is Xw -> S -> H -> copy -> Yc.
 //
 // Roundings to 16 bits: M and the H copy, once each (the operands of y, which
 // is itself rounded to 16 bits).  The state is not: Xw, a product of an fp32
-// weight and a 16-bit input, goes through the tensor core as three 16-bit
-// pieces whose sum is Xw to 24 bits, against the exact B, and H lives in fp32
-// registers.  For fp16 the pieces are formed of Xw times a power of two that
-// puts the chunk's largest product below 2^15 (undone exactly on S), so that
-// small values do not fall out of fp16's range.
+// weight and a 16-bit input, goes through the tensor core as 16-bit pieces,
+// against the exact B, and H lives in fp32 registers.  Three pieces of bf16 hold
+// 24 bits; two of fp16 hold 22, with an error of at most 2^-22 of the product,
+// and are formed of Xw times a power of two that puts the chunk's largest
+// product below 2^15 (undone exactly on S), so that small values do not fall out
+// of fp16's range.
 //
 // Decays.  Exponents are formed from sums inside blocks of 32 tokens and the
 // blocks' totals, never as differences of long prefix sums, so a strong decay
@@ -48,30 +49,34 @@
 // element.
 //
 // Work split.  The chunks of all (sequence, head pair) units, in order, are
-// cut into equal contiguous ranges, one per block; a planning kernel finds the
-// cuts from the lengths in device memory.  A unit that a cut falls into is
-// handed over: the block that has its first part runs that part first and
-// publishes the state; the block with its last part runs that part last.  A
-// block whose whole range lies inside one unit first runs its state products
-// alone from zero, then adds the published state of the block before, decayed,
-// publishes the sum and runs its range in full.  Blocks take their number from
-// a counter, so a block only ever waits for one that has started; the wait is
-// bounded all the same, as every wait here is: one that runs out sets a bit of
-// the fault word and the block drains its copies and products and leaves.
+// cut into contiguous ranges of equal cost, one per block; a planning kernel
+// finds the cuts from the lengths in device memory.  A unit that a cut falls
+// into is handed over: the block that has its first part runs that part first
+// and publishes the state; a block whose whole range lies inside the unit first
+// runs its state products alone, from zero, and publishes that state and its
+// decay.  Neither waits for anyone.  Then such a block, and the one with the
+// last part (as its last run), sums the published states before its own, each
+// decayed over the ranges between, and runs its range in full.  (Handing one sum
+// on from block to block took 215 us for 32768 tokens x 24 heads, 25 of them in
+// the chain; this takes 185.)  Blocks take their number from a counter, so a
+// block only ever waits for one that has started; the wait is bounded all the
+// same, as every wait here is: one that runs out sets a bit of the fault word
+// and the block drains its copies and products and leaves.
 //
 // What bounds it: the matrix instructions it needs (26 MFLOP per chunk and
 // pair at N = 128, half of them for the exact state) are 75 us at the rate of a
 // large bf16 product for 4 x 4096 tokens x 80 heads, its bytes 57 us; measured
-// 166 us on B200 (0.78 PFLOP/s, 2.2 TB/s), 224 us for one sequence of 32768
-// tokens x 24 heads, 235 us for 8192 tokens of ragged prompts x 80 heads with
-// their states, 17 us for one prompt of 37 tokens.  The rest is the chain
+// 170 us on B200 (0.76 PFLOP/s, 2.2 TB/s), 185 us for one sequence of 32768
+// tokens x 24 heads in fp16, 146 us for 8192 tokens of ragged prompts x 80 heads
+// with their states, 17 us for one prompt of 37 tokens.  The rest is the chain
 // above, and the issue slots of Xw: its warps work 7 of a chunk's 9 thousand
-// cycles.  What made the difference on the way, at the 4 x 4096 x 80 size: one
-// group of 8 warps that does everything in turn 338 us; copies and products in
-// warps of their own 242; the state's warps apart from y's 234; two operand
-// buffers for S and the copy written on the way 212; rolled loops and short
-// waits, which keep the hot code of all roles (30 KB) inside the instruction
-// cache, 179; the gate compiled apart and accumulators given back early 166.
+// cycles.  What made the difference on the way: at 4 x 4096 x 80, one group of 8
+// warps that does everything in turn 338 us, copies and products in warps of
+// their own 242, the state's warps apart from y's 234, two operand buffers for S
+// and the copy written on the way 212, rolled loops and short waits, which keep
+// what the roles run most inside the instruction cache, 179, the gate compiled
+// apart and accumulators given back early 166; ragged, a block barrier behind
+// every run 237, flowing from run to run 204, ranges of equal cost 146.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -109,14 +114,16 @@ struct Cut {
 };
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 struct PlanLayout {
-  size_t prefix, cuts, flags, carry, total;
+  size_t prefix, cuts, flags, decay, carry, total;
 };
 __host__ __device__ inline PlanLayout plan_layout(int64_t nseq, int blocks, int dstate) {
   PlanLayout l;
   l.prefix = 0;                                              // long long [nseq + 1]: cost before sequence i
   l.cuts = align256((nseq + 1) * sizeof(long long));         // Cut [blocks + 1]
   l.flags = l.cuts + align256((blocks + 1) * sizeof(Cut));   // unsigned [blocks], then the counter
-  l.carry = l.flags + align256((blocks + 1) * sizeof(unsigned));
+  // float [blocks][2]: log2 decay over the published run
+  l.decay = l.flags + align256((blocks + 1) * sizeof(unsigned));
+  l.carry = l.decay + align256(blocks * 2 * sizeof(float));
   l.total = l.carry + (size_t)blocks * 2 * kP * dstate * sizeof(float);
   return l;
 }
@@ -239,15 +246,15 @@ enum : int {
   kBarT = 22,     // y's accumulators are read
   kBarE = 23,     // S is read: the next chunk's products may start
   kBarN = 24,     // [kRuns] a run is found
-  kBarD = 28,     // [kRuns] a run is done in the warps of all roles but the planning one
+  kBarD = 28,     // [kRuns] a run is done in all warps
   kNumBars = 32
 };
 constexpr int kRuns = 4;  // runs known at a time
 __host__ __device__ constexpr unsigned arrivals(int i) {
-  return i < kBarW || (i >= kBarN && i < kBarD) ? 1  // the thread in charge
-         : i >= kBarD                          ? kThreads / 32
-         : i == kBarM || (i >= kBarY && i <= kBarT) ? 8  // the warps of the y group
-                                               : 4;  // those of the state's or Xw's
+  return i < kBarW || (i >= kBarN && i < kBarD)     ? 1  // the thread in charge
+         : i >= kBarD                               ? kThreads / 32
+         : i == kBarM || (i >= kBarY && i <= kBarT) ? 8   // the warps of the y group
+                                                    : 4;  // those of the state's or Xw's
 }
 
 __device__ __forceinline__ uint32_t swz(int r, int c) {
@@ -312,8 +319,8 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 // A run of a block: a unit, its chunks [c0, c0 + n), where its state comes from
 // and goes to.  n < 0: there are no more.
 struct Run {
-  int seq, c0, n, begin, end, slot, g, h0, nh2;
-  bool full, from_slot, from_carry, awaited, publish, to_slot;
+  int seq, pair, c0, n, begin, end, slot, g, h0, nh2;
+  bool full, from_slot, from_carry, publish, to_slot;
   __device__ __forceinline__ int t0(int j) const { return begin + (c0 + j) * kQ; }
 };
 
@@ -347,17 +354,17 @@ struct Runs {
     int stage = this->stage, useq = this->useq, upair = this->upair, seen = this->seen, slot = this->slot;
     __syncwarp();
     while (stage < 6) {
-      int pair, c1 = -1;
+      int c1 = -1;
       run.full = run.from_slot = true;
-      run.from_carry = run.awaited = run.publish = run.to_slot = false;
+      run.from_carry = run.publish = run.to_slot = false;
       if (stage <= 1) {         // inside one unit: the range's own state, from zero; then in full
-        run.seq = A.seq; pair = A.pair; run.c0 = A.chunk; c1 = E.chunk;
+        run.seq = A.seq; run.pair = A.pair; run.c0 = A.chunk; c1 = E.chunk;
         run.from_slot = false;
-        run.full = run.from_carry = run.awaited = stage == 1;
+        run.full = run.from_carry = stage == 1;
         run.publish = stage == 0;
         stage = stage == 0 ? 1 : 6;
       } else if (stage == 2) {  // the first part of the unit at the range's end
-        run.seq = E.seq; pair = E.pair; run.c0 = 0; c1 = E.chunk;
+        run.seq = E.seq; run.pair = E.pair; run.c0 = 0; c1 = E.chunk;
         run.publish = true;
         stage = same ? 6 : 3;
       } else if (stage == 3) {  // whole units
@@ -365,11 +372,11 @@ struct Runs {
           stage = A.chunk > 0 ? 4 : 6;
           continue;
         }
-        run.seq = useq; pair = upair; run.c0 = 0;
+        run.seq = useq; run.pair = upair; run.c0 = 0;
         run.to_slot = true;
         if (++upair == npairs) { upair = 0; ++useq; }
       } else {                  // the last part of the unit at the range's start
-        run.seq = A.seq; pair = A.pair; run.c0 = A.chunk;
+        run.seq = A.seq; run.pair = A.pair; run.c0 = A.chunk;
         run.from_slot = false;
         run.from_carry = run.to_slot = true;
         stage = 6;
@@ -388,8 +395,8 @@ struct Runs {
       run.end = seq_end(p.seq, run.seq, run.begin);
       if (c1 < 0) c1 = (run.end - run.begin + kQ - 1) / kQ;
       run.n = c1 - run.c0;  // 0 for an empty sequence: the state passes through
-      run.g = pair / ppg;
-      run.h0 = run.g * per + 2 * (pair - run.g * ppg);
+      run.g = run.pair / ppg;
+      run.h0 = run.g * per + 2 * (run.pair - run.g * ppg);
       run.nh2 = min(2, run.g * per + per - run.h0);  // an odd group's last pair holds one head
       break;
     }
@@ -462,13 +469,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   char* const ws = static_cast<char*>(p.ws);
   const PlanLayout play = plan_layout(p.seq.nseq, blocks, N);
   unsigned* const flags = reinterpret_cast<unsigned*>(ws + play.flags);
+  const Cut* const cuts = reinterpret_cast<const Cut*>(ws + play.cuts);
+  float* const decay = reinterpret_cast<float*>(ws + play.decay);
   float4* const carry = reinterpret_cast<float4*>(ws + play.carry);
   if (warp == kTmaWarp) {
     unsigned b = 0;
     if (lane == 0) b = atomicAdd(flags + blocks, 1u);
     b = __shfl_sync(0xffffffffu, b, 0);
     if (lane == 0) s_block = b;
-    if (lane == 0) s_runs.start(p, reinterpret_cast<const Cut*>(ws + play.cuts) + b, npairs);
+    if (lane == 0) s_runs.start(p, cuts + b, npairs);
   }
   __syncthreads();
   const int me = (int)s_block;
@@ -645,28 +654,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------- the state -------
       const bool owns = hrow < nh2;
       const int stid = tid - kGroupY;
-      auto wait_flag = [&]() {  // the state that the block before publishes
+      auto wait_flag = [&](int b) {  // the state that block b publishes
         if (stid == 0) {
           uint32_t polls = 0, v = 0;
           do {
-            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flags + me - 1) : "memory");
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flags + b) : "memory");
           } while (!v && ++polls < kFlagLimit);
           if (!v) ok = false;
         }
         return !sync_s(!ok);
       };
-      const float4* const src = carry + (size_t)(me - 1) * (2 * kP * N / 4);
       // ---- the state entering the run
       float hs[N];
       float* st = p.state && owns ? p.state + (((size_t)run->slot * p.nheads + h0) * kP + row) * N : nullptr;
 #pragma unroll
       for (int i = 0; i < N; ++i) hs[i] = 0.f;
-      if (run->from_carry) {
-        if (!run->awaited) wait_flag();
+      if (run->from_carry) {  // the unit's runs before this one, each decayed over those between, back to its first
+        float between = 0.f;
+#pragma unroll 1
+        for (int b = me - 1; b >= 0 && wait_flag(b); --b) {
+          const float4* const src = carry + (size_t)b * (2 * kP * N / 4);
+          const float dec = ex2(between);
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-          const float4 v = __ldcg(src + i * kGroupS + stid);
-          hs[4 * i] = v.x; hs[4 * i + 1] = v.y; hs[4 * i + 2] = v.z; hs[4 * i + 3] = v.w;
+          for (int i = 0; i < N / 4; ++i) {
+            const float4 v = __ldcg(src + i * kGroupS + stid);
+            hs[4 * i] = fmaf(dec, v.x, hs[4 * i]);
+            hs[4 * i + 1] = fmaf(dec, v.y, hs[4 * i + 1]);
+            hs[4 * i + 2] = fmaf(dec, v.z, hs[4 * i + 2]);
+            hs[4 * i + 3] = fmaf(dec, v.w, hs[4 * i + 3]);
+          }
+          const Cut c = cuts[b];
+          if (c.seq != run->seq || c.pair != run->pair || c.chunk == 0) break;
+          between += __ldcg(decay + 2 * b + hrow);
         }
       } else if (run->from_slot && st && !(p.slots.fresh && p.slots.fresh[run->seq])) {
 #pragma unroll
@@ -719,25 +738,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         signal(kBarE);
         if (more) signal(kBarH + ((k + 1) & 1));
       }
-      ok = !sync_s(!ok);
-
       // ---- the state leaving the run
-      if (!full && ok && wait_flag()) {  // the middle of a unit: add what enters it, decayed
-        const float dec = ex2(psum);
-#pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-          const float4 v = __ldcg(src + i * kGroupS + stid);
-          hs[4 * i] = fmaf(dec, v.x, hs[4 * i]);
-          hs[4 * i + 1] = fmaf(dec, v.y, hs[4 * i + 1]);
-          hs[4 * i + 2] = fmaf(dec, v.z, hs[4 * i + 2]);
-          hs[4 * i + 3] = fmaf(dec, v.w, hs[4 * i + 3]);
-        }
-      }
       if (run->publish) {
         float4* dst = carry + (size_t)me * (2 * kP * N / 4);
 #pragma unroll
         for (int i = 0; i < N / 4; ++i)
           dst[i * kGroupS + stid] = make_float4(hs[4 * i], hs[4 * i + 1], hs[4 * i + 2], hs[4 * i + 3]);
+        if ((stid & 63) == 0) decay[2 * me + hrow] = psum;
         __threadfence();
         sync_s(false);
         if (stid == 0) asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(flags + me) : "memory");
