@@ -229,3 +229,51 @@ def test_two_streams_with_their_own_workspaces():
             got.append(ops.ssd_prefill(**q, **kw))
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in got)
+
+
+@pytest.mark.parametrize("dtype,nh,ng,N,gate", [("bf16", 5, 1, 128, True), ("f16", 6, 2, 64, False), ("bf16", 12, 4, 64, True)])
+def test_many_prompts_per_block(dtype, nh, ng, N, gate):
+    """More (sequence, head pair) units than blocks, so that a block goes through several of every kind: whole
+    ones of one chunk or more, parts, empty ones, skipped ones, pairs that hold one head."""
+    g = torch.Generator().manual_seed(nh)
+    lens = torch.randint(0, 260, (130,), generator=g)
+    lens[torch.randperm(130, generator=g)[:25]] = 0
+    lens[17] = 1500
+    cu = cu_of(lens.tolist())
+    tokens = int(lens.sum())
+    gd, q, kw = make(tokens + 9, nh, ng, N, dtype, 71 + nh, slice_rows=True)
+    if not gate:
+        kw["z"] = None
+    slots = torch.randperm(140, generator=g)[:130].to(torch.int32)
+    slots[torch.randperm(130, generator=g)[:12]] = -1
+    fresh = torch.rand(130, generator=g) < 0.5
+    slots, fresh = slots.to(DEV), fresh.to(DEV)
+    state = torch.randn(140, nh, 64, N, device=DEV, generator=gd)
+    r = ref.ssd(**q, **kw, cu=cu, state=state, slots=slots, fresh=fresh)
+    out = torch.full((tokens + 9, nh, 64), 7.0, device=DEV, dtype=q["x"].dtype)
+    start = state.clone()
+    y = ops.ssd_prefill(**q, **kw, cu_seqlens=cu, state=state, slots=slots, fresh=fresh, out=out)
+    check(y, state, r, q["x"].dtype)
+    assert (y.cpu()[~r["covered"]] == 7).all()
+    again = start.clone()
+    y2 = ops.ssd_prefill(**q, **kw, cu_seqlens=cu, state=again, slots=slots, fresh=fresh)
+    k = r["covered"]
+    assert torch.equal(y.cpu()[k], y2.cpu()[k]) and torch.equal(state, again)
+
+
+@pytest.mark.parametrize("dtype,nh,N", [("bf16", 2, 128), ("f16", 1, 64)])
+def test_a_long_prompt_among_short_ones(dtype, nh, N):
+    """The long one's chunks go to some twenty blocks, most of which hold nothing else: each sums the states of
+    all before it."""
+    lens = [40] * 15 + [6000] + [40] * 15
+    cu = cu_of(lens)
+    g, q, kw = make(sum(lens), nh, 1, N, dtype, 91)
+    q["A"] = q["A"] * 1e-3      # slow decay: what the first blocks publish reaches the last
+    state = torch.randn(len(lens), nh, 64, N, device=DEV, generator=g)
+    r = ref.ssd(**q, **kw, cu=cu, state=state)
+    start = state.clone()
+    y = ops.ssd_prefill(**q, **kw, cu_seqlens=cu, state=state)
+    check(y, state, r, q["x"].dtype)
+    again = start.clone()
+    y2 = ops.ssd_prefill(**q, **kw, cu_seqlens=cu, state=again)
+    assert torch.equal(y, y2) and torch.equal(state, again)
