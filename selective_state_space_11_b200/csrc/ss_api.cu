@@ -854,10 +854,12 @@ void conv_tm_strips(int64_t tokens, int* strip, int* nstrip) {
   *nstrip = (int)((tokens + len - 1) / len);
 }
 
-// Backward blocks per column group: about two per SM of a 148-SM device in all.
+// Backward blocks per column group: one per SM of a 148-SM device in all, which
+// a block's registers fill.  Two took 169 us against 163 at 16384 x 5120 bf16,
+// 68 against 61 at 16384 x 1536: twice the weights to load and sums to write.
 int norm_blocks(int64_t rows, int64_t dim, int64_t group, int slots) {
   const int64_t ngroups = dim / group;
-  int64_t cap = 296 / ngroups;
+  int64_t cap = 148 / ngroups;
   if (cap < 1) cap = 1;
   const int64_t need = (rows + slots - 1) / slots;
   return (int)(need < cap ? need : cap);

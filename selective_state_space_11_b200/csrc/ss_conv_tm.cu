@@ -25,8 +25,8 @@
 // the token axis whatever the sequences.  dx[t] needs dpre[t .. t+W-1], so a
 // strip recomputes dpre for W-1 tokens behind it.  dw and dbias stay in
 // registers over the strip, go to one partial per strip, and a second kernel
-// sums the strips in order: no atomics, bitwise reproducible.  139 us at the
-// same size (529 MB, 3.8 TB/s).  W + 1 products and the SiLU' of every token
+// sums the strips in order: no atomics, bitwise reproducible.  132 us at the
+// same size (529 MB, 4.0 TB/s; the second kernel starts under the first).  W + 1 products and the SiLU' of every token
 // are formed, then 2 W more for dw and dx, 30 instructions an element: the fp32
 // pipe and its latency bound it.  One token at a time, masked wherever it is, it
 // took 191 us and 45 instructions; 5 blocks per SM, in 96 registers, 170.
@@ -358,6 +358,7 @@ struct Walk {
 
 template <typename T, int V, int W, bool SILU>
 __global__ void __launch_bounds__(128) conv_tm_bwd_kernel(const ConvTmParams p) {
+  pdl_trigger();
   if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, &g_fault_conv_tm);
   const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
   if (c >= p.dim) return;
@@ -553,7 +554,9 @@ __global__ void __launch_bounds__(256) conv_tm_reduce_kernel(const ConvTmParams 
   const int n = p.dim * (p.width + 1);
   const int j = blockIdx.x * 32 + lane;
   float a = 0.f;
+  pdl_wait();
   if (j < n)
+#pragma unroll 8
     for (int s = row; s < p.nstrip; s += 8) a += p.part[(size_t)s * n + j];
   sh[row][lane] = a;
   __syncthreads();
@@ -600,8 +603,8 @@ cudaError_t run(const ConvTmParams& p, bool backward, int sms, cudaStream_t s) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  conv_tm_reduce_kernel<<<(unsigned)(((long long)p.dim * (W + 1) + 31) / 32), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_behind(conv_tm_reduce_kernel, (unsigned)(((long long)p.dim * (W + 1) + 31) / 32), 256, 0, s,
+                       p);
 }
 
 template <typename T, int V>

@@ -262,4 +262,21 @@ cudaError_t read_fault_conv_tm(unsigned* bits, bool clear);
 cudaError_t read_fault_step(unsigned* bits, bool clear);
 cudaError_t read_fault_prefill(unsigned* bits, bool clear);
 
+// Launches a kernel that may start while the one before it in the stream still
+// runs (programmatic stream serialisation); it waits with pdl_wait().
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 }  // namespace ss

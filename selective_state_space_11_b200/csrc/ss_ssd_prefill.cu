@@ -1132,17 +1132,7 @@ cudaError_t run(const SsdPrefillParams& p, cudaStream_t s) {
   const int smem = Lay<N>::kAlloc;
   e = cudaFuncSetAttribute(prefill_tc_kernel<T, N, GATE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_tc_kernel<T, N, GATE>, p, npairs, blocks, mx, mb, mc, my);
+  return launch_behind(prefill_tc_kernel<T, N, GATE>, blocks, kThreads, smem, s, p, npairs, blocks, mx, mb, mc, my);
 }
 
 template <typename T>

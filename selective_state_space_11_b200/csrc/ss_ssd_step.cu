@@ -128,17 +128,9 @@ cudaError_t run_t(const SsdStepParams& p, cudaStream_t s) {
     case 4: e = run_conv<T, 4>(p, s); break;
   }
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.nheads, p.batch);
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return p.dstate == 128 ? cudaLaunchKernelEx(&cfg, step_state_kernel<T, 128>, p)
-                         : cudaLaunchKernelEx(&cfg, step_state_kernel<T, 64>, p);
+  const dim3 grid(p.nheads, p.batch);
+  return p.dstate == 128 ? launch_behind(step_state_kernel<T, 128>, grid, 128, 0, s, p)
+                         : launch_behind(step_state_kernel<T, 64>, grid, 128, 0, s, p);
 }
 
 }  // namespace
