@@ -468,6 +468,7 @@ SS_API ss_status ss_state_update(int64_t batch, int64_t dim, int64_t dstate, int
  *     and sets bit 3 of ss_device_fault: no two sequences ever share a state in
  *     a call.  fresh (nseq,) uint8, or NULL: nonzero starts the sequence from
  *     a zero state instead of its slot's.  Only slots in use are read or written.
+ *     slots and fresh go with a cache: without one they are refused.
  *   - Launches depend on the arguments' sizes only, never on device data: the
  *     calls capture into CUDA graphs, and a replay follows the data then in
  *     cu_seqlens, slots and fresh.

@@ -814,6 +814,8 @@ ss_status check_ragged(const char* fn, int64_t tokens, int64_t nseq, const int32
     if (slots && !aligned(slots, 4)) return fail(SS_ERR_ALIGNMENT, "%s: slots not 4-byte aligned", fn);
     c->index = slots;
     c->count = (int)nslots;
+  } else if (slots) {
+    return fail(SS_ERR_INVALID_ARG, "%s: slots given without a cache", fn);
   }
   return SS_OK;
 }
@@ -891,6 +893,7 @@ ss_status ss_conv1d_tm_fwd(int64_t tokens, int64_t nseq, int64_t dim, int64_t wi
   const size_t es = elt_size(dtype);
   if ((st = check_rows(fn, "x", x, ldx, dim, es, tokens)) != SS_OK) return st;
   if (nslots != 0 && width > 1 && !state) return fail(SS_ERR_INVALID_ARG, "%s: nslots given without state", fn);
+  if (nslots == 0 && (state || fresh)) return fail(SS_ERR_INVALID_ARG, "%s: state or fresh given without nslots", fn);
   if (!w || (tokens > 0 && (!y0 || (dim1 && !y1) || (dim2 && !y2))))
     return fail(SS_ERR_INVALID_ARG, "%s: w and an output per piece are required", fn);
   for (const void* q : {(const void*)y0, (const void*)y1, (const void*)y2})
@@ -1147,6 +1150,8 @@ ss_status ss_ssd_prefill(int64_t tokens, int64_t nseq, int64_t nheads, int64_t h
   if ((st = check_rows(fn, "C", C, ldc, gn, es, tokens)) != SS_OK) return st;
   if (z && (st = check_rows(fn, "z", z, ldz, d, es, tokens)) != SS_OK) return st;
   if (!A || (tokens > 0 && !y)) return fail(SS_ERR_INVALID_ARG, "%s: A and y are required", fn);
+  if (!state && (nslots != 0 || fresh))
+    return fail(SS_ERR_INVALID_ARG, "%s: nslots or fresh given without state", fn);
   // x, B and C are operand tiles of the tensor cores: their rows start on 16-byte boundaries
   for (auto q : {std::make_pair(x, ldx), std::make_pair(B, ldb), std::make_pair(C, ldc)})
     if (!vec_rows(q.first, q.second, es))

@@ -26,10 +26,11 @@
 // strip recomputes dpre for W-1 tokens behind it.  dw and dbias stay in
 // registers over the strip, go to one partial per strip, and a second kernel
 // sums the strips in order: no atomics, bitwise reproducible.  132 us at the
-// same size (529 MB, 4.0 TB/s; the second kernel starts under the first).  W + 1 products and the SiLU' of every token
-// are formed, then 2 W more for dw and dx, 30 instructions an element: the fp32
-// pipe and its latency bound it.  One token at a time, masked wherever it is, it
-// took 191 us and 45 instructions; 5 blocks per SM, in 96 registers, 170.
+// same size (529 MB, 4.0 TB/s; the second kernel starts under the first).  W + 1
+// products and the SiLU' of every token are formed, then 2 W more for dw and
+// dx, 30 instructions an element: the fp32 pipe and its latency bound it.  One
+// token at a time, masked wherever it is, it took 191 us and 45 instructions; 5
+// blocks per SM, in 96 registers, 170.
 #include <type_traits>
 
 #include "ss_device.cuh"

@@ -680,6 +680,8 @@ def conv1d_tm_fwd(x, w, bias=None, splits=None, cu_seqlens=None, state=None, slo
     nslots = 0
     if state is not None:
         nslots = state.shape[0]
+        if nslots == 0 and nseq > 0:
+            raise ValueError("the state cache has no slots")
         _is(state, "state", (nslots, dim, W - 1), torch.float32, dev)
     elif slots is not None or fresh is not None:
         raise ValueError("slots and fresh go with a state cache")
@@ -746,7 +748,9 @@ class _CausalConv1dTm(torch.autograd.Function):
 
 def causal_conv1d_tm_fn(x, w, bias=None, splits=None, cu_seqlens=None, silu=True):
     """Differentiable conv1d_tm_fwd (no cache): a tuple of pieces; x (tokens, dim) or
-    (batch, L, dim).  Rows of no sequence are zero, and so are their gradients."""
+    (batch, L, dim).  Rows of no sequence are zero, and so are their gradients.  For a
+    step in a CUDA graph, capture conv1d_tm_fwd and conv1d_tm_bwd themselves: torch
+    cannot capture a backward pass of leaves that an eager graph still holds."""
     return _CausalConv1dTm.apply(x, w, bias, splits, cu_seqlens, silu)
 
 
@@ -778,6 +782,8 @@ def ssd_prefill(x, dt, A, B, C, state=None, D=None, z=None, dt_bias=None, dt_sof
     nslots = 0
     if state is not None:
         nslots = state.shape[0]
+        if nslots == 0 and nseq > 0:
+            raise ValueError("the state cache has no slots")
         _is(state, "state", (nslots, nh, P, N), torch.float32, dev)
     elif slots is not None or fresh is not None:
         raise ValueError("slots and fresh go with a state cache")
@@ -912,7 +918,8 @@ class _GatedNorm(torch.autograd.Function):
 
 
 def gated_norm_fn(x, z, w, group=None, eps=1e-5, gate_last=False):
-    """Differentiable gated_norm_fwd: returns y."""
+    """Differentiable gated_norm_fwd: returns y.  For a step in a CUDA graph, capture
+    gated_norm_fwd and gated_norm_bwd themselves (as for causal_conv1d_tm_fn)."""
     return _GatedNorm.apply(x, z, w, group, eps, gate_last)
 
 

@@ -66,6 +66,12 @@ BAD = [
     ("ss_conv1d_tm_fwd", dict(y2=P + 1), ALIGNMENT),
     ("ss_conv1d_tm_fwd", dict(bias=P + 2), ALIGNMENT),
     ("ss_conv1d_tm_fwd", dict(cu=P + 2), ALIGNMENT),
+    ("ss_conv1d_tm_fwd", dict(nslots=0), INVALID),                     # slots without a cache
+    ("ss_conv1d_tm_fwd", dict(nslots=0, slots=None, fresh=None), INVALID),
+    ("ss_conv1d_tm_fwd", dict(nslots=0, slots=None, state=None), INVALID),
+    ("ss_ssd_prefill", dict(state=None), INVALID),
+    ("ss_ssd_prefill", dict(state=None, slots=None, nslots=0), INVALID),
+    ("ss_ssd_prefill", dict(state=None, slots=None, fresh=None), INVALID),
     ("ss_conv1d_tm_bwd", dict(ldx=8), INVALID),
     ("ss_conv1d_tm_bwd", dict(lddx=8), INVALID),
     ("ss_conv1d_tm_bwd", dict(dy0=None), INVALID),
