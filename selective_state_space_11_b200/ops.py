@@ -657,7 +657,7 @@ def _check_conv_tm(x, w, bias, splits, cu_seqlens):
     tokens, nseq = _ragged(lead, cu_seqlens, dev)
     _is(w, "w", (dim, W), torch.float32, dev)
     _is(bias, "bias", (dim,), torch.float32, dev, optional=True)
-    splits = (dim,) if splits is None else tuple(int(s) for s in splits)
+    splits = (dim,) if splits is None else tuple(splits)
     if not 1 <= len(splits) <= 3 or sum(splits) != dim or min(splits) <= 0:
         raise ValueError(f"splits {splits}: one to three positive widths that sum to {dim}")
     return dev, lead, tokens, nseq, dim, W, ldx, splits
@@ -687,11 +687,12 @@ def conv1d_tm_fwd(x, w, bias=None, splits=None, cu_seqlens=None, state=None, slo
         raise ValueError("slots and fresh go with a state cache")
     fresh = _slot_args(nseq, slots, fresh, dev)
     if out is None:
-        out = tuple(torch.empty(*lead, s, device=dev, dtype=x.dtype) for s in splits)
-    if len(out) != len(splits):
-        raise ValueError(f"out holds {len(out)} pieces, expected {len(splits)}")
-    for i, (o, s) in enumerate(zip(out, splits)):
-        _is(o, f"out[{i}]", lead + (s,), x.dtype, dev)
+        out = [x.new_empty(lead + (s,)) for s in splits]
+    else:
+        if len(out) != len(splits):
+            raise ValueError(f"out holds {len(out)} pieces, expected {len(splits)}")
+        for i, (o, s) in enumerate(zip(out, splits)):
+            _is(o, f"out[{i}]", lead + (s,), x.dtype, dev)
     d = splits + (0,) * (3 - len(splits))
     y = tuple(out) + (None,) * (3 - len(splits))
     with _On(dev) as stream:
@@ -713,10 +714,10 @@ def conv1d_tm_bwd(x, w, dy, bias=None, cu_seqlens=None, silu=True, dx=None,
     for i, (t, s) in enumerate(zip(dy, splits)):
         _is(t, f"dy[{i}]", lead + (s,), x.dtype, dev)
     if dx is None:
-        dx = torch.empty(*lead, dim, device=dev, dtype=x.dtype)
-    lddx = _need_rows(dx, "dx", lead, (dim,), x.dtype, dev)
-    f32 = dict(device=dev, dtype=torch.float32)
-    g = dict(dx=dx, dw=torch.empty(dim, W, **f32), dbias=torch.empty(dim, **f32))
+        dx, lddx = x.new_empty(x.shape), dim
+    else:
+        lddx = _need_rows(dx, "dx", lead, (dim,), x.dtype, dev)
+    g = dict(dx=dx, dw=w.new_empty(w.shape), dbias=w.new_empty(dim))
     d = splits + (0,) * (3 - len(splits))
     t = tuple(dy) + (None,) * (3 - len(splits))
     with _On(dev) as stream:
@@ -788,8 +789,9 @@ def ssd_prefill(x, dt, A, B, C, state=None, D=None, z=None, dt_bias=None, dt_sof
     elif slots is not None or fresh is not None:
         raise ValueError("slots and fresh go with a state cache")
     fresh = _slot_args(nseq, slots, fresh, dev)
-    y = out if out is not None else torch.empty(*lead, nh, P, device=dev, dtype=x.dtype)
-    _is(y, "out", lead + (nh, P), x.dtype, dev)
+    y = x.new_empty(x.shape) if out is None else out
+    if out is not None:
+        _is(y, "out", x.shape, x.dtype, dev)
     with _On(dev) as stream:
         workspace = _ws(lib().ss_ssd_prefill_workspace_size(tokens, nseq, nh, P, ng, N), workspace, dev)
         size = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -829,8 +831,9 @@ def ssd_step(xbc, dt, w, A, conv_state, state, conv_bias=None, D=None, z=None, d
     _is(conv_state, "conv_state", (nslots, dim, W - 1), torch.float32, dev)
     _is(state, "state", (nslots, nh, P, N), torch.float32, dev)
     _slot_args(bsz, slots, None, dev)
-    y = out if out is not None else torch.empty(bsz, nh, P, device=dev, dtype=xbc.dtype)
-    _is(y, "out", (bsz, nh, P), xbc.dtype, dev)
+    y = xbc.new_empty((bsz, nh, P)) if out is None else out
+    if out is not None:
+        _is(y, "out", (bsz, nh, P), xbc.dtype, dev)
     with _On(dev) as stream:
         workspace = _ws(lib().ss_ssd_step_workspace_size(bsz, nh, P, ngroups, N), workspace, dev)
         size = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -868,9 +871,10 @@ def gated_norm_fwd(x, z, w, group=None, eps=1e-5, gate_last=False, want_rstd=Tru
     most 8192).  rstd (..., dim / group) fp32 is what gated_norm_bwd takes.
     """
     dev, lead, rows, dim, group, ldx, ldz = _check_norm(x, z, w, group)
-    y = out if out is not None else torch.empty(*lead, dim, device=dev, dtype=x.dtype)
-    _is(y, "out", lead + (dim,), x.dtype, dev)
-    rstd = torch.empty(*lead, dim // group, device=dev, dtype=torch.float32) if want_rstd else None
+    y = x.new_empty(x.shape) if out is None else out
+    if out is not None:
+        _is(y, "out", x.shape, x.dtype, dev)
+    rstd = w.new_empty(lead + (dim // group,)) if want_rstd else None
     with _On(dev) as stream:
         _check(lib().ss_gated_norm_fwd(rows, dim, group, _DTYPE[x.dtype], _at(x), ldx, _at(z), ldz, _at(w),
                                        float(eps), int(bool(gate_last)), _at(y), _at(rstd), stream))
@@ -887,12 +891,11 @@ def gated_norm_bwd(x, z, w, dy, rstd, group=None, gate_last=False, dx=None, dz=N
     _is(rstd, "rstd", lead + (dim // group,), torch.float32, dev)
     if z is None and dz is not None:
         raise ValueError("dz given without z")
-    new = dict(device=dev, dtype=x.dtype)
-    dx = torch.empty(*lead, dim, **new) if dx is None else dx
-    dz = torch.empty(*lead, dim, **new) if dz is None and z is not None else dz
+    dx = x.new_empty(x.shape) if dx is None else dx
+    dz = x.new_empty(x.shape) if dz is None and z is not None else dz
     lddx = _need_rows(dx, "dx", lead, (dim,), x.dtype, dev)
     lddz = 0 if dz is None else _need_rows(dz, "dz", lead, (dim,), x.dtype, dev)
-    dw = torch.empty(dim, device=dev, dtype=torch.float32)
+    dw = w.new_empty(dim)
     with _On(dev) as stream:
         workspace = _ws(lib().ss_gated_norm_bwd_workspace_size(rows, dim, group), workspace, dev)
         size = 0 if workspace is None else workspace.numel() * workspace.element_size()
