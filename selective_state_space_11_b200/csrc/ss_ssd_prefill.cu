@@ -58,7 +58,7 @@
 // last part (as its last run), sums the published states before its own, each
 // decayed over the ranges between, and runs its range in full.  (Handing one sum
 // on from block to block took 215 us for 32768 tokens x 24 heads, 25 of them in
-// the chain; this takes 185.)  Blocks take their number from a counter, so a
+// the chain; summing took 185.)  Blocks take their number from a counter, so a
 // block only ever waits for one that has started; the wait is bounded all the
 // same, as every wait here is: one that runs out sets a bit of the fault word
 // and the block drains its copies and products and leaves.
@@ -66,7 +66,7 @@
 // What bounds it: the matrix instructions it needs (26 MFLOP per chunk and
 // pair at N = 128, half of them for the exact state) are 75 us at the rate of a
 // large bf16 product for 4 x 4096 tokens x 80 heads, its bytes 57 us; measured
-// 170 us on B200 (0.76 PFLOP/s, 2.2 TB/s), 185 us for one sequence of 32768
+// 170 us on B200 (0.76 PFLOP/s, 2.2 TB/s), 175 us for one sequence of 32768
 // tokens x 24 heads in fp16, 146 us for 8192 tokens of ragged prompts x 80 heads
 // with their states, 17 us for one prompt of 37 tokens.  The rest is the chain
 // above, and the issue slots of Xw: its warps work 7 of a chunk's 9 thousand
@@ -97,13 +97,19 @@ namespace {
 
 constexpr int kP = 64;         // head dimension
 constexpr int kQ = 128;        // chunk length
-// Warps: 0-7 the y group, 8-11 the state's, 12-15 Xw's, then the helpers.  The
-// registers of a block, 96 per thread at launch, are split unevenly: a thread
-// of the state's warps holds a whole state row.
+// Warps: 0-7 the y group, 8-11 the state's, 12-15 Xw's, then the helpers.
 constexpr int kGroupY = 256, kGroupS = 128;  // threads of the y group, of the state's and Xw's
 constexpr int kMmaY = 16, kMmaS = 17, kTmaWarp = 18;  // and 19, the decays
 constexpr int kThreads = 640;
-constexpr int kRegsS = 168, kRegsX = 64, kRegsHelp = 56;  // 2 x 96 + 168 + 64 + 56 = 5 x 96 per quarter of the SM
+// The registers of a block, 96 per thread at launch, are split unevenly: a
+// thread of the state's warps holds a whole state row.  What a row of 64 leaves
+// goes to Xw's warps and the helpers: 175 us for 32768 tokens x 24 heads, where
+// the split of 128 took 185.  Sums: 2 x 96 + S + X + Help <= 5 x 96.
+template <int N>
+struct Regs {
+  static constexpr int kS = N == 64 ? 112 : 168, kX = N == 64 ? 88 : 64, kHelp = N == 64 ? 88 : 56;
+  static_assert(2 * 96 + kS + kX + kHelp <= 5 * 96, "a split above the launch's registers would wait forever");
+};
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr uint32_t kFlagLimit = 1u << 22;  // polls of a predecessor's flag
 constexpr uint32_t kG = 0, kYc = 128, kM = 256, kS = 384;  // TMEM columns (Ym over G)
@@ -647,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       done(r);
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsS));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(Regs<N>::kS));
     for (uint32_t r = 0; next(r, sync_s); ++r) {
       const int n = run->n, h0 = run->h0, nh2 = run->nh2;
       const bool full = run->full;
@@ -755,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       done(r);
     }
   } else if (warp < 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsX));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(Regs<N>::kX));
     // ----------------------------------------------------------------- Xw
     // a warp: 32 columns of head xh, lanes over tokens
     const int stid = tid - kGroupY - kGroupS, xh = blk >> 1, xc = 4 * (blk & 1);
@@ -813,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           unsigned char* const to = sm + L::kW + (q & 1) * 24576 + xh * 4096;
           // the products of the quarter before the last have read the buffer
           if (q > 1 || k > 0) wait(kBarS + (q & 1), q > 1 ? 0 : 1);
-#pragma unroll 2
+#pragma unroll(N == 64 ? 4 : 2)  // as far as the registers go
           for (int k4 = xc; k4 < xc + 4; ++k4) {
             uint4* const xp = reinterpret_cast<uint4*>(from + swz(32 * q + lane, k4));
             if (!live) *xp = make_uint4(0, 0, 0, 0);
@@ -855,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       done(r);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsHelp));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(Regs<N>::kHelp));
     if (warp == kTmaWarp) {
       // y of the last two chunks in full, to be stored when its buffer is needed
       // or at the end (t < 0: a ragged chunk, whose y the y group writes)
