@@ -66,7 +66,7 @@
 // What bounds it: the matrix instructions it needs (26 MFLOP per chunk and
 // pair at N = 128, half of them for the exact state) are 75 us at the rate of a
 // large bf16 product for 4 x 4096 tokens x 80 heads, its bytes 57 us; measured
-// 170 us on B200 (0.76 PFLOP/s, 2.2 TB/s), 175 us for one sequence of 32768
+// 170 us on B200 (0.76 PFLOP/s, 2.2 TB/s), 171 us for one sequence of 32768
 // tokens x 24 heads in fp16, 146 us for 8192 tokens of ragged prompts x 80 heads
 // with their states, 17 us for one prompt of 37 tokens.  The rest is the chain
 // above, and the issue slots of Xw: its warps work 7 of a chunk's 9 thousand
@@ -103,7 +103,7 @@ constexpr int kMmaY = 16, kMmaS = 17, kTmaWarp = 18;  // and 19, the decays
 constexpr int kThreads = 640;
 // The registers of a block, 96 per thread at launch, are split unevenly: a
 // thread of the state's warps holds a whole state row.  What a row of 64 leaves
-// goes to Xw's warps and the helpers: 175 us for 32768 tokens x 24 heads, where
+// goes to Xw's warps and the helpers: 171 us for 32768 tokens x 24 heads, where
 // the split of 128 took 185.  Sums: 2 x 96 + S + X + Help <= 5 x 96.
 template <int N>
 struct Regs {
@@ -808,6 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // sequence belong to others, and a missing head has none: no NaN of
         // theirs may meet a zero weight, so x, and with its last rows B, become zero there.
         const int xval = xh < nh2 ? nval : 0;
+        constexpr int kAhead = N == 64 ? 4 : 2;  // vectors of x at a time, as far as the registers go
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           float later = 0.f;  // log2 decay of the blocks behind
@@ -819,31 +820,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           unsigned char* const to = sm + L::kW + (q & 1) * 24576 + xh * 4096;
           // the products of the quarter before the last have read the buffer
           if (q > 1 || k > 0) wait(kBarS + (q & 1), q > 1 ? 0 : 1);
-#pragma unroll(N == 64 ? 4 : 2)  // as far as the registers go
-          for (int k4 = xc; k4 < xc + 4; ++k4) {
-            uint4* const xp = reinterpret_cast<uint4*>(from + swz(32 * q + lane, k4));
-            if (!live) *xp = make_uint4(0, 0, 0, 0);
-            const uint4 xv = *xp;
-            const uint32_t in[4] = {xv.x, xv.y, xv.z, xv.w};
-            uint32_t u[4], v[4], z[4];
+#pragma unroll 1
+          for (int k0 = xc; k0 < xc + 4; k0 += kAhead) {
+            uint4 xv[kAhead];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = Pk<T>::unpack(in[e]);
-              const f2_t x0 = mul2(pk2(f.x, f.y), w2);
-              u[e] = Pk<T>::pack(lo2(x0), hi2(x0));
-              const float2 f0 = Pk<T>::unpack(u[e]);
-              const f2_t x1 = fma2(pk2(f0.x, f0.y), minus, x0);
-              v[e] = Pk<T>::pack(lo2(x1), hi2(x1));
-              if (kPieces == 3) {
-                const float2 f1 = Pk<T>::unpack(v[e]);
-                const f2_t x2 = fma2(pk2(f1.x, f1.y), minus, x1);
-                z[e] = Pk<T>::pack(lo2(x2), hi2(x2));
-              }
+            for (int i = 0; i < kAhead; ++i) {
+              uint4* const xp = reinterpret_cast<uint4*>(from + swz(32 * q + lane, k0 + i));
+              if (!live) *xp = make_uint4(0, 0, 0, 0);
+              xv[i] = *xp;
             }
-            const uint32_t o = swz(lane, k4);
-            *reinterpret_cast<uint4*>(to + o) = make_uint4(u[0], u[1], u[2], u[3]);
-            *reinterpret_cast<uint4*>(to + 8192 + o) = make_uint4(v[0], v[1], v[2], v[3]);
-            if (kPieces == 3) *reinterpret_cast<uint4*>(to + 16384 + o) = make_uint4(z[0], z[1], z[2], z[3]);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+              const int k4 = k0 + i;
+              const uint32_t in[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
+              uint32_t u[4], v[4], z[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = Pk<T>::unpack(in[e]);
+                const f2_t x0 = mul2(pk2(f.x, f.y), w2);
+                u[e] = Pk<T>::pack(lo2(x0), hi2(x0));
+                const float2 f0 = Pk<T>::unpack(u[e]);
+                const f2_t x1 = fma2(pk2(f0.x, f0.y), minus, x0);
+                v[e] = Pk<T>::pack(lo2(x1), hi2(x1));
+                if (kPieces == 3) {
+                  const float2 f1 = Pk<T>::unpack(v[e]);
+                  const f2_t x2 = fma2(pk2(f1.x, f1.y), minus, x1);
+                  z[e] = Pk<T>::pack(lo2(x2), hi2(x2));
+                }
+              }
+              const uint32_t o = swz(lane, k4);
+              *reinterpret_cast<uint4*>(to + o) = make_uint4(u[0], u[1], u[2], u[3]);
+              *reinterpret_cast<uint4*>(to + 8192 + o) = make_uint4(v[0], v[1], v[2], v[3]);
+              if (kPieces == 3) *reinterpret_cast<uint4*>(to + 16384 + o) = make_uint4(z[0], z[1], z[2], z[3]);
+            }
           }
           if (32 * q + 32 > nval) {
             wait(kBarB, k);
