@@ -118,17 +118,6 @@ __device__ __forceinline__ bool wait_until(uint32_t bar, uint32_t parity, uint32
       : "memory");
   return n < limit;
 }
-// Whether the phase with the given parity has completed; does not block.
-__device__ __forceinline__ bool test(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done;
-}
 
 // 4-d tiled bulk tensor copy global -> shared, completion on an mbarrier.
 // The tensor map must describe memory of this GPU; no multicast.
