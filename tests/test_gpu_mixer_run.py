@@ -265,3 +265,37 @@ def test_an_injected_launch_failure_is_reported_and_enqueues_nothing(name, monke
     monkeypatch.delenv("SS_FAIL_LAUNCH")
     calls[name]()
     torch.cuda.synchronize()
+
+
+def test_offsets_beyond_32_bits():
+    """Rows a million elements apart and slots far into a cache of states, so that both pass 2^31 elements: the
+    results of dense rows and a small cache."""
+    m = Layer(4, 1, 128, 256, 23)
+    tokens, far = 2200, (1 << 31) // (4 * 64 * 128) + 3
+    dense = m.rows(tokens)
+    wide = torch.empty(tokens, 1 << 20, device=DEV, dtype=m.dtype)[:, :m.width]
+    wide.copy_(dense)
+    grads = torch.empty(tokens, 1 << 20, device=DEV, dtype=m.dtype)[:, :m.width]
+    cu = i32(0, 1500, tokens)
+    win, state = m.caches(2)
+    big_state = torch.empty(far, 4, 64, 128, device=DEV)
+    big_win = torch.empty(far, m.dim, 3, device=DEV)
+    big_state[-2:], big_win[-2:] = state, win
+    here, there = i32(0, 1), i32(far - 2, far - 1)
+
+    def run(row, w, s, slots, gz, gx):
+        got = m.prompts(row, cu, w, s, slots, None)
+        one = m.token(row[:2], w, s, slots)
+        z, xbc, _ = m.cut(row)
+        y = got["y"].flatten(1)
+        out, rstd = ops.gated_norm_fwd(y, z, m.norm_w, group=m.group)
+        n = ops.gated_norm_bwd(y, z, m.norm_w, out, rstd, group=m.group, dz=gz)
+        c = ops.conv1d_tm_bwd(xbc, m.w, [n["dx"], got["B"].flatten(1), got["C"].flatten(1)], m.bias, cu_seqlens=cu, dx=gx)
+        return [got["y"], got["out"], one["y"], one["out"], out, n["dx"], n["dw"], c["dw"], c["dbias"]]
+
+    small = torch.empty_like(dense)
+    a = run(dense, win, state, here, m.cut(small)[0], m.cut(small)[1])
+    b = run(wide, big_win, big_state, there, m.cut(grads)[0], m.cut(grads)[1])
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    assert torch.equal(big_state[-2:], state) and torch.equal(big_win[-2:], win)
+    assert all(torch.equal(u, v) for u, v in zip(m.cut(small)[:2], m.cut(grads)[:2]))
