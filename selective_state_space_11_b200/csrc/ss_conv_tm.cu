@@ -222,8 +222,9 @@ template <typename T, int V, int W>
 __global__ void __launch_bounds__(128) conv_tm_fwd_kernel(const ConvTmParams p, int tile) {
   if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.seq, &g_fault_conv_tm);
   const RaggedTile rt = ragged_tile(p.seq, blockIdx.x, tile);
+  // no tile of a sequence: ahead of the first one's first, or behind a sequence's last
+  if (rt.k < 0 || (rt.k > 0 && (long long)rt.k * tile >= rt.end - rt.begin)) return;
   const int s = rt.begin + rt.k * tile;
-  if (rt.k > 0 && s >= rt.end) return;
   int slot = -1;
   if (p.slots.count > 0) {
     slot = claim_slot(p.slots, rt.seq, &g_fault_conv_tm);

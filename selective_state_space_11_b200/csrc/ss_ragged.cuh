@@ -23,12 +23,14 @@ __device__ __forceinline__ int seq_end(const Ragged& r, int i, int begin) {
 // floor(begin_i / tile) + i on.  Its ceil(len_i / tile) tiles (at least one,
 // also when it is empty) fit before those of i + 1, so
 // floor(tokens / tile) + nseq numbers are enough, and a number finds its sequence by bisection.
-// Numbers behind a sequence's last tile give k >= its tile count.
+// Numbers behind a sequence's last tile give k >= its tile count, and those
+// ahead of sequence 0's first tile, where the offsets start above 0, k < 0:
+// the caller leaves both out.
 __host__ __device__ __forceinline__ long long ragged_tiles(const Ragged& r, int tile) {
   return r.nseq > 0 ? (long long)r.tokens / tile + r.nseq : 0;
 }
 struct RaggedTile {
-  int seq, k;      // sequence, tile within it
+  int seq, k;      // sequence, tile within it (of no sequence: k < 0 or >= its tile count)
   int begin, end;  // the whole sequence's tokens
 };
 __device__ __forceinline__ RaggedTile ragged_tile(const Ragged& r, long long v, int tile) {
