@@ -488,14 +488,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const int me = (int)s_block;
 
-  // A wait that runs out makes the thread's `ok` false: it waits for nothing
-  // any more, and its role leaves its loop where all of the role's warps can.
+  // A wait that runs out makes the warp's `ok` false: it waits for nothing any
+  // more, and its role leaves its loop where all of the role's warps can.  `ok`
+  // is the same in all lanes where a whole warp waits; wait_lane is for one lane.
   bool ok = true;
   auto wait = [&](int i, uint32_t parity) {
-    if (ok) ok = tc::wait_until(bar(i), parity & 1u, kWaitLimit);
+    if (ok) ok = tc::wait_warp(bar(i), parity & 1u, kWaitLimit);
+  };
+  auto wait_lane = [&](int i, uint32_t parity) {
+    if (ok) ok = tc::wait(bar(i), parity & 1u, kWaitLimit);
   };
   // the pairs that alternate between chunks
   auto wait2 = [&](int i, uint32_t k) { wait(i + (int)(k & 1), k >> 1); };
+  auto wait2_lane = [&](int i, uint32_t k) { wait_lane(i + (int)(k & 1), k >> 1); };
   // barriers that the copy and the product thread have armed, and the parity
   // of the last phase, for the drain
   uint32_t armed = 0, last_par = 0, next_par = 0;
@@ -668,7 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           } while (!v && ++polls < kFlagLimit);
           if (!v) ok = false;
         }
-        return !sync_s(!ok);
+        ok = !sync_s(!ok);
+        return ok;
       };
       // ---- the state entering the run
       float hs[N];
@@ -918,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t = run->t0(j);
           if (lane == 0 && ok) {  // each buffer as its last reader is done
             if (full) {
-              if (kf > 1) wait2(kBarY, kf - 2);
+              if (kf > 1) wait2_lane(kBarY, kf - 2);
               if (ok) store_y(t_a, h_a, k);
               t_a = t_b;
               h_a = h_b;
@@ -928,20 +934,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (ok) load(kBarX + (k & 1), L::kX + (k & 1) * 32768, &map_x, h0 * kP, t, nh2);
             if (full) {
-              if (kf > 0) wait(kBarYc, kf - 1);
+              if (kf > 0) wait_lane(kBarYc, kf - 1);
               if (ok) load(kBarC, L::kC, &map_c, run->g * N, t, N / 64);
             }
-            if (k > 0) wait2(kBarSall, k - 1);
+            if (k > 0) wait2_lane(kBarSall, k - 1);
             if (ok) load(kBarB, L::kB, &map_b, run->g * N, t, N / 64);
           }
-          __syncwarp();
+          ok = __all_sync(0xffffffffu, ok);
         }
         done(r);
       }
       if (lane == 0) {
-        if (itf > 1) wait2(kBarY, itf - 2);
+        if (itf > 1) wait2_lane(kBarY, itf - 2);
         if (ok) store_y(t_a, h_a, it);
-        if (itf > 0) wait2(kBarY, itf - 1);
+        if (itf > 0) wait2_lane(kBarY, itf - 1);
         if (ok) store_y(t_b, h_b, it + 1);
       }
     } else if (warp == kMmaY) {

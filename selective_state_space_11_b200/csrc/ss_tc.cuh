@@ -105,17 +105,19 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint32_t lim
   return false;
 }
 
-// The same wait as a few instructions in one place (code that many warps walk
-// through once in a while has to fit the instruction cache).
-__device__ __forceinline__ bool wait_until(uint32_t bar, uint32_t parity, uint32_t limit) {
-  uint32_t n;
-  asm volatile(
-      "{\n .reg .pred p, q;\n mov.u32 %0, 0;\n"
-      "W: mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra.uni D;\n"
-      " add.u32 %0, %0, 1;\n setp.lt.u32 q, %0, %3;\n @q bra.uni W;\nD:\n}\n"
-      : "=&r"(n)
-      : "r"(bar), "r"(parity), "r"(limit)
-      : "memory");
+// The same wait of a whole warp.  Each lane polls for itself and the phase may
+// complete between two lanes' polls, so the lanes vote: they leave together,
+// with one answer, ready for the instructions that all lanes execute as one.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, uint32_t limit) {
+  uint32_t n = 0, done;
+  do {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  } while (!__all_sync(0xffffffffu, done) && ++n < limit);
   return n < limit;
 }
 
