@@ -528,9 +528,12 @@ SS_API size_t ss_ssd_prefill_workspace_size(int64_t tokens, int64_t nseq, int64_
  * headdim 64, dstate 64 or 128 (else SS_ERR_UNSUPPORTED).  Rows of x, B and C
  * start on 16-byte boundaries (a multiple of 8 elements apart); y is 16-byte,
  * state 32-byte and the workspace 256-byte aligned (else SS_ERR_ALIGNMENT).
- * The state is accurate to fp32.  y takes one 16-bit rounding of the masked
- * products (C_i . B_j) decay Delta_j and of the state entering a run of 128
- * tokens, on top of its own: in fp16 these overflow, in y alone, above 65504.
+ * The state is accurate to fp32: its products (decay Delta x) . B are formed of
+ * 24 bits of the left factor in bf16, in fp16 of 22 bits or 2^-39 of the largest
+ * one in the head's run of 128 tokens, whichever is more.  y takes one 16-bit
+ * rounding of the masked products (C_i . B_j) decay Delta_j and of the state
+ * entering a run of 128 tokens, on top of its own: in fp16 these overflow, in y
+ * alone, above 65504.
  * Decays are meant to be at most 1 (A <= 0, Delta >= 0); growth works until
  * fp32 overflows inside 128 tokens.  A NaN or an infinity in x, B, C or dt of a token may
  * reach y of up to 127 tokens before it in its own sequence (one tile of the

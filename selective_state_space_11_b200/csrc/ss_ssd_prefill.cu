@@ -36,10 +36,13 @@
 // is itself rounded to 16 bits).  The state is not: Xw, a product of an fp32
 // weight and a 16-bit input, goes through the tensor core as 16-bit pieces,
 // against the exact B, and H lives in fp32 registers.  Three pieces of bf16 hold
-// 24 bits; two of fp16 hold 22, with an error of at most 2^-22 of the product,
-// and are formed of Xw times a power of two that puts the chunk's largest
-// product below 2^15 (undone exactly on S), so that small values do not fall out
-// of fp16's range.
+// 24 bits.  Two of fp16 hold 22, and are formed of Xw times a power of two that
+// puts the largest of the chunk and head into [2^14, 2^15) (undone exactly on S),
+// so that a growing state does not leave fp16's range and small values do not
+// fall out of it: each is within 2^-22 of itself or 2^-39 of the largest.  The
+// largest is taken of the weighted products, decay to the chunk's end included:
+// of |x| Delta alone, growth by more than 2 in a chunk made the state NaN, and a
+// token that a later one makes the state forget set the scale for all.
 //
 // Decays.  Exponents are formed from sums inside blocks of 32 tokens and the
 // blocks' totals, never as differences of long prefix sums, so a strong decay
@@ -782,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait2(kBarX, k);
         wait2(kBarA, k);
         float scale = 1.f;
-        if constexpr (!kBf16) {  // fp16: the power of two that puts max (|x| Delta) below 2^15
+        if constexpr (!kBf16) {  // fp16: the power of two that puts max |Xw| into [2^14, 2^15)
           if (stid < 2) sMax[stid] = 0u;
           sync_x(false);
 #pragma unroll 1
@@ -794,18 +797,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               const unsigned m0 = __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu);
               m = __vmaxu2(m, __vmaxu2(m0, __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
             }
-            m = max(m & 0xffffu, m >> 16);
-            float top = __half2float(__ushort_as_half((unsigned short)m)) * fabsf(a.dl[e][row]);
-            top = top < 3.0e38f ? top : 1.f;
-            if (row >= nval || e >= nh2) top = 0.f;
+            m = min(max(m & 0xffffu, m >> 16), 0x7bffu);  // (an infinity or a NaN stays one, and sets no scale)
+            // the weight as below: the decay up to the chunk's end takes part
+            const float4 tot = *reinterpret_cast<const float4*>(a.tot[e]);
+            const float later = (blk < 1 ? tot.y : 0.f) + (blk < 2 ? tot.z : 0.f) + (blk < 3 ? tot.w : 0.f);
+            float top = __half2float(__ushort_as_half((unsigned short)m)) * fabsf(a.f[e][row] * ex2(later));
+            top = row < nval && e < nh2 ? fminf(top, 3.0e38f) : 0.f;
 #pragma unroll
             for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             if (lane == 0) atomicMax(sMax + e, __float_as_uint(top));
           }
           sync_x(false);
-          auto power = [](unsigned v) {  // 2^(14 - exponent of v), within fp32's range
+          auto power = [](unsigned v) {  // 2^(14 - exponent of v), so that it and its inverse are fp32 numbers
             const int e = (int)(v >> 23) - 127;
-            return v == 0 ? 0 : min(100, max(-100, 14 - e));
+            return v == 0 ? 0 : min(126, 14 - e);
           };
           scale = __uint_as_float((unsigned)(127 + power(sMax[xh])) << 23);
           if (stid < 2) sUn[2 * (k & 1) + stid] = __uint_as_float((unsigned)(127 - power(sMax[stid])) << 23);
@@ -819,7 +824,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 4; ++q) {
           float later = 0.f;  // log2 decay of the blocks behind
           for (int b = q + 1; b < 4; ++b) later += a.tot[xh][b];
-          const float w = a.f[xh][32 * q + lane] * ex2(later) * scale;
+          float w = a.f[xh][32 * q + lane] * ex2(later);
+          if constexpr (!kBf16) {  // finite weights stay finite: a token of zeros has no part in the scale
+            const float ws = w * scale;
+            w = fabsf(w) <= 3.0e38f ? fminf(fmaxf(ws, -3.0e38f), 3.0e38f) : ws;
+          }
           const f2_t w2 = pk2(w, w), minus = pk2(-1.f, -1.f);
           unsigned char* const from = xs + xh * 16384;
           const bool live = 32 * q + lane < xval;
