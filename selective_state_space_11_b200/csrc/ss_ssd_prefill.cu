@@ -49,7 +49,10 @@
 // loses no bits: exp(cs_i - cs_j) for j in an earlier block is
 // exp(from the end of j's block to i) x exp(from j to the end of its block),
 // both at most 1 for A < 0, and only the diagonal blocks take an exponential per
-// element.
+// element, of a difference of sums inside the block.  There a token's log2 decay
+// counts down to kForget, whose power of two is 0 in fp32 as that of any below
+// is: else the sums of the tokens behind one that resets the state lose the bits
+// that set them apart (a decay of e^-40000 left y 11 half steps of fp16 off).
 //
 // Work split.  The chunks of all (sequence, head pair) units, in order, are
 // cut into contiguous ranges of equal cost, one per block; a planning kernel
@@ -115,6 +118,7 @@ struct Regs {
 };
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr uint32_t kFlagLimit = 1u << 22;  // polls of a predecessor's flag
+constexpr float kForget = -160.f;
 constexpr uint32_t kG = 0, kYc = 128, kM = 256, kS = 384;  // TMEM columns (Ym over G)
 
 // Workspace: the plan, then the published states.
@@ -1057,7 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Arrays& a = arr[k & 1];
           const int t = run->t0(j) + 4 * lane, left = run->end - t;
           const T* const dtg = static_cast<const T*>(p.dt) + h;
-          f2_t d[4], in[4];
+          f2_t d[4], ld[4], in[4];  // ld: a token's log2 decay
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const T* const at = dtg + (int64_t)min(t + i, run->end - 1) * p.lddt;
@@ -1072,7 +1076,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (p.softplus) d[i] = pk2(softplus_f(lo2(d[i])), softplus_f(hi2(d[i])));
             if (i >= left) d[i] = zero;
             if (h1 == 0) d[i] = pk2(lo2(d[i]), 0.f);
-            in[i] = i ? fma2(d[i], A2, in[i - 1]) : mul2(d[i], A2);
+            const f2_t e = mul2(d[i], A2);
+            ld[i] = pk2(lo2(e) < kForget ? kForget : lo2(e), hi2(e) < kForget ? kForget : hi2(e));
+            in[i] = i ? add2(in[i - 1], ld[i]) : ld[i];
           }
           f2_t before = in[3], after = in[3];
 #pragma unroll
@@ -1090,9 +1096,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (seg == 7) v = zero;
           f2_t f[4];  // from the token to the end of its block
           f[3] = v;
-          f[2] = fma2(d[3], A2, zero);
-          f[1] = fma2(d[2], A2, f[2]);
-          f[0] = add2(fma2(d[1], A2, f[1]), v);
+          f[2] = ld[3];
+          f[1] = add2(ld[2], f[2]);
+          f[0] = add2(add2(ld[1], f[1]), v);
           f[1] = add2(f[1], v);
           f[2] = add2(f[2], v);
 #pragma unroll

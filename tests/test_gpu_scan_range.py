@@ -107,3 +107,22 @@ def test_sums_of_every_size(dtype, nh, N, dexp, xexp):
     q["dt"][:] = 2.0 ** dexp
     q["x"][70], q["dt"][70] = 0.0, 2.0 ** 15
     run(q, torch.zeros(nh, device=DEV), state * 2.0 ** (dexp + xexp), dtype, "state")
+
+
+@pytest.mark.parametrize("dtype,nh,N", SHAPES)
+@pytest.mark.parametrize("big", [10.0, 500.0, 1e4, 6e4])
+@pytest.mark.parametrize("where", [(0,), (35,), (62, 63), (64, 100, 127, 128)])
+def test_y_behind_a_reset(dtype, nh, N, big, where):
+    """Tokens that decay the state by e^-20 to e^-240000 between ordinary ones.  A block of 32 tokens holds at most two,
+    which count for at most 160 each in its sums of log2 decays: below 512, where a rounding is off by at most 2^-16.
+    An exponent is the difference of two sums of at most 8 such roundings each: 16 x 2^-16 x ln 2 < 2900 x 2^-24 of its
+    exponential, beside the 1024 of the recurrence."""
+    g, q, state = make(150, nh, N, dtype, 71)
+    q["dt"][list(where)] = big
+    A = -2.0 * (1.0 + torch.arange(nh, device=DEV))
+    r = ref.ssd(**q, A=A, softplus=False, state=state)
+    y = ops.ssd_prefill(**q, A=A, dt_softplus=False, state=state)
+    extra = ref.half_step(TYPES[dtype]) * r["mag"]
+    if dtype == "f16":  # the smallest half step, of M and of the state's copy
+        extra = extra + 2.0 ** -25 * (ref.f64(q["x"]).abs().amax() * 128 + ref.f64(q["C"]).abs().sum(2).amax())
+    ref.assert_within(y, r["y"], r["mag"], TYPES[dtype], "y", 4 * 1024, extra=extra)
