@@ -538,8 +538,11 @@ SS_API size_t ss_ssd_prefill_workspace_size(int64_t tokens, int64_t nseq, int64_
  * fp32 overflows inside 128 tokens.  A NaN or an infinity in x, B, C or dt of a token may
  * reach y of up to 127 tokens before it in its own sequence (one tile of the
  * tensor cores); earlier and other sequences' tokens are never reached.
- * Waits inside the kernel are bounded: one that runs out sets bits 1 or 2 of
- * ss_device_fault.
+ * Waits inside the kernel are bounded: one that runs out sets bit 1 of
+ * ss_device_fault, and bit 2 if copies or products were still in flight after
+ * another such wait at exit; y and the states of the call mean nothing then.
+ * Test hook: with SS_INJECT_WAIT_TIMEOUT set, a wait of each block's first run
+ * of 128 tokens runs out.
  */
 SS_API ss_status ss_ssd_prefill(int64_t tokens, int64_t nseq, int64_t nheads, int64_t headdim,
                                 int64_t ngroups, int64_t dstate, int dtype, const void* x, int64_t ldx,

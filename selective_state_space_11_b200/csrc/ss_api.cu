@@ -1172,6 +1172,7 @@ ss_status ss_ssd_prefill(int64_t tokens, int64_t nseq, int64_t nheads, int64_t h
   p.softplus = dt_softplus ? 1 : 0;
   p.x = x; p.ldx = ldx; p.dt = dt; p.lddt = lddt; p.B = B; p.ldb = ldb; p.C = C; p.ldc = ldc; p.z = z; p.ldz = ldz;
   p.zvec = vec_rows(z, ldz, es) ? 1 : 0;
+  p.inject_timeout = std::getenv("SS_INJECT_WAIT_TIMEOUT") != nullptr;
   p.A = A; p.D = D; p.dt_bias = dt_bias; p.state = state; p.y = y; p.ws = workspace;
   if (launch_injected())
     return fail(SS_ERR_CUDA, "%s: launch failure injected by SS_FAIL_LAUNCH (nothing enqueued)", fn);

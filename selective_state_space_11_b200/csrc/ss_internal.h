@@ -237,6 +237,7 @@ struct SsdPrefillParams {
   Slots slots;
   int nheads, headdim, ngroups, dstate, softplus;
   int zvec;                   // rows of z start on 16-byte boundaries
+  int inject_timeout;         // test hook: a wait of the first chunk runs out
   const void *x, *dt, *B, *C, *z;  // (tokens, ...) rows ldx, lddt, ldb, ldc, ldz apart; z may be null
   int64_t ldx, lddt, ldb, ldc, ldz;
   const float *A, *D, *dt_bias;

@@ -116,7 +116,10 @@ struct Regs {
   static constexpr int kS = N == 64 ? 112 : 168, kX = N == 64 ? 88 : 64, kHelp = N == 64 ? 88 : 56;
   static_assert(2 * 96 + kS + kX + kHelp <= 5 * 96, "a split above the launch's registers would wait forever");
 };
-constexpr uint32_t kWaitLimit = 1u << 22;
+// Polls of a wait.  One that fails has blocked for 4 us (measured, of a lane and
+// of 1 to 20 warps alike), so a wait gives up after a second; what it is for
+// takes microseconds, and a predecessor's state 2 us for each chunk of its range.
+constexpr uint32_t kWaitLimit = 1u << 18;
 constexpr uint32_t kFlagLimit = 1u << 22;  // polls of a predecessor's flag
 constexpr float kForget = -160.f;
 constexpr uint32_t kG = 0, kYc = 128, kM = 256, kS = 384;  // TMEM columns (Ym over G)
@@ -997,6 +1000,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             arm(kBarG + e);
           }
+          // test hook (SS_INJECT_WAIT_TIMEOUT): y's accumulators, which hold nothing yet, are not read
+          if (p.inject_timeout && kf == 0) ok = ok && tc::wait_warp(bar(kBarT), 0, 1u << 12);
           wait2(kBarX, k);
           wait(kBarM, kf);
           if (run->t0(j + 1) > run->end) wait2(kBarR, k);  // a ragged chunk's x is cleared behind its end
