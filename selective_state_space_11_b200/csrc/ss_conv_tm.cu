@@ -25,10 +25,11 @@
 // the token axis whatever the sequences.  dx[t] needs dpre[t .. t+W-1], so a
 // strip recomputes dpre for W-1 tokens behind it.  dw and dbias stay in
 // registers over the strip, go to one partial per strip, and a second kernel
-// sums the strips in order: no atomics, bitwise reproducible.  132 us at the
+// sums the strips in order: no atomics, bitwise reproducible.  131 us at the
 // same size (529 MB, 4.0 TB/s; the second kernel starts under the first).  W + 1
 // products and the SiLU' of every token are formed, then 2 W more for dw and
-// dx, 30 instructions an element: the fp32 pipe and its latency bound it.  One
+// dx, 30 instructions an element.  Neither pipe is full (issue slots 58%, HBM
+// 62%): latency bounds it, with the 16 warps that 128 registers leave an SM.  One
 // token at a time, masked wherever it is, it took 191 us and 45 instructions; 5
 // blocks per SM, in 96 registers, 170.
 #include <type_traits>
@@ -62,7 +63,7 @@ __device__ __forceinline__ uint32_t word_of(float lo, float hi) {
   }
 }
 
-// V elements of a row as loaded: 16 bytes (V > 1) or one element.
+// V elements of a row as loaded: 4 (8 bytes of a 16-bit type, 16 of fp32) or one.
 template <typename T, int V>
 struct Raw {
   static constexpr int kWords = V * (int)sizeof(T) / 4;

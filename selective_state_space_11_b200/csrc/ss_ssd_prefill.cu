@@ -33,7 +33,13 @@
 // is updated, so the chain from chunk to chunk is Xw -> S -> H -> copy -> Yc.
 //
 // Roundings to 16 bits: M and the H copy, once each (the operands of y, which
-// is itself rounded to 16 bits).  The state is not: Xw, a product of an fp32
+// is itself rounded to 16 bits).  Against 64 bits y is then 2.05e-3 off in bf16
+// and 2.5e-4 in fp16 where its own rounding alone leaves 1.66e-3 and 2.1e-4;
+// nearly all of the difference is M's.  M in two pieces (the second in G's columns,
+// M X added to the scaled Yc) brings it to 1.67e-3 and 2.1e-4, but takes 213 us
+// for 169 (4 x 4096 x 80), 177 for 147 (ragged) and 218 for 178 (32768 x 24): the
+// y warps' issue slots, which Xw's warps need.  So one rounding each, as in
+// ss_ssd_fwd.  The state is not rounded: Xw, a product of an fp32
 // weight and a 16-bit input, goes through the tensor core as 16-bit pieces,
 // against the exact B, and H lives in fp32 registers.  Three pieces of bf16 hold
 // 24 bits.  Two of fp16 hold 22, and are formed of Xw times a power of two that
@@ -71,18 +77,22 @@
 //
 // What bounds it: the matrix instructions it needs (26 MFLOP per chunk and
 // pair at N = 128, half of them for the exact state) are 75 us at the rate of a
-// large bf16 product for 4 x 4096 tokens x 80 heads, its bytes 57 us; measured
-// 170 us on B200 (0.76 PFLOP/s, 2.2 TB/s), 171 us for one sequence of 32768
-// tokens x 24 heads in fp16, 146 us for 8192 tokens of ragged prompts x 80 heads
-// with their states, 17 us for one prompt of 37 tokens.  The rest is the chain
+// large bf16 product for 4 x 4096 tokens x 80 heads, its bytes 57 us.  Measured
+// on B200, in a graph replayed on one state, part of which stays in L2: 169 us
+// (0.76 PFLOP/s), 177 us for one sequence of 32768 tokens x 24 heads in fp16, 148
+// us for 8192 tokens of ragged prompts x 80 heads with their states, 16.5 us for
+// one prompt of 37 tokens.  On three states in turn 4 x 4096 x 80 takes 174 to 181
+// us, in a loop of seconds, at the power limit, 188.  With a gate z it is 306, and
+// 236 ragged: a thread reads a token's row of z by itself.  The rest is the chain
 // above, and the issue slots of Xw: its warps work 7 of a chunk's 9 thousand
 // cycles.  What made the difference on the way: at 4 x 4096 x 80, one group of 8
 // warps that does everything in turn 338 us, copies and products in warps of
 // their own 242, the state's warps apart from y's 234, two operand buffers for S
 // and the copy written on the way 212, rolled loops and short waits, which keep
-// what the roles run most inside the instruction cache, 179, the gate compiled
-// apart and accumulators given back early 166; ragged, a block barrier behind
-// every run 237, flowing from run to run 204, ranges of equal cost 146.
+// what the roles run most inside the instruction cache, 179 (a look at a stop flag
+// in every wait's loop: 218 for 169), the gate compiled apart and accumulators
+// given back early 166; ragged, a block barrier behind every run 237, flowing from
+// run to run 204, ranges of equal cost 146.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -109,7 +119,7 @@ constexpr int kMmaY = 16, kMmaS = 17, kTmaWarp = 18;  // and 19, the decays
 constexpr int kThreads = 640;
 // The registers of a block, 96 per thread at launch, are split unevenly: a
 // thread of the state's warps holds a whole state row.  What a row of 64 leaves
-// goes to Xw's warps and the helpers: 171 us for 32768 tokens x 24 heads, where
+// goes to Xw's warps and the helpers: 176 us for 32768 tokens x 24 heads, where
 // the split of 128 took 185.  Sums: 2 x 96 + S + X + Help <= 5 x 96.
 template <int N>
 struct Regs {
