@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const unsigned m0 = __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu);
               m = __vmaxu2(m, __vmaxu2(m0, __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
             }
-            m = min(max(m & 0xffffu, m >> 16), 0x7bffu);  // (an infinity or a NaN stays one, and sets no scale)
+            m = min(max(m & 0xffffu, m >> 16), 0x7bffu);  // (an infinity or a NaN counts as the largest number)
             // the weight as below: the decay up to the chunk's end takes part
             const float4 tot = *reinterpret_cast<const float4*>(a.tot[e]);
             const float later = (blk < 1 ? tot.y : 0.f) + (blk < 2 ? tot.z : 0.f) + (blk < 3 ? tot.w : 0.f);
